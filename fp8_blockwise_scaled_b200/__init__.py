@@ -19,6 +19,16 @@ Layouts (row-major, dimensions multiples of 128):
   fp8blk_quantize_weight_128x128_both(w[N,K]) -> q, s, qT, sT from one read of w
   fp8blk_gemm(layout, a[M,K], sa[K/128,M], b[N,K], sb) -> d[M,N] bfloat16
       sb = [N/128,K/128] for FWD/DGRAD, [K/128,N] for WGRAD
+
+Rows sorted by group (tokens sorted by expert; offsets: int32 [groups + 1] on the device, any
+number of rows in a group):
+  fp8blk_quantize_act_1x128_grouped(x[T,C], offsets, mode)
+      ROWWISE   -> q_row[T,C], s_row[C/128,T];  COLWISE_T -> q_colT[C,P], s_colT[P/128,C],
+      P = fp8blk_grouped_padded_rows(T, groups): whole 128-token blocks for every group
+  fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets)
+      FWD  : a[T,in],  b = q[groups*out,in]            -> Y[T,out]
+      DGRAD: a[T,out], b = qT[in,groups*out]           -> dX[T,in]
+      WGRAD: a[out,P], b[in,P]                         -> dW[groups,out,in]
 """
 from __future__ import annotations
 
@@ -26,7 +36,7 @@ import ctypes
 
 import torch
 
-from ._lib import (A_E5M2, B_E5M2, BOTH, COLWISE_T, DGRAD, E5M2, FWD, MAX_WEIGHTS, OUT_F32, ROWWISE, WGRAD,
+from ._lib import (A_E5M2, B_E5M2, BOTH, COLWISE_T, DGRAD, E5M2, FWD, MAX_GROUPS, MAX_WEIGHTS, OUT_F32, ROWWISE, WGRAD,
                    Fp8BlkError, LIB_PATH, WeightDesc, check, lib, status_string)
 
 __all__ = [
@@ -35,7 +45,8 @@ __all__ = [
     "fp8blk_amax_ema_static", "AMAX_EMA_STATIC_MAX_ROWS",
     "fp8blk_quantize_tensor", "fp8blk_gemm_tensor_scaled", "fp8_linear_delayed_forward",
     "fp8blk_gemm", "fp8blk_gemm_splitk", "fp8blk_gemm_splitk_count", "fp8blk_gemm_splitk_workspace_bytes", "fp8blk_round_f32_to_bf16", "fp8blk_get_device_error", "fp8blk_version", "linear_forward",
-    "linear_backward", "ROWWISE", "COLWISE_T", "BOTH", "E5M2", "FWD", "DGRAD", "WGRAD", "A_E5M2", "B_E5M2",
+    "linear_backward", "fp8blk_grouped_padded_rows", "fp8blk_quantize_act_1x128_grouped", "fp8blk_gemm_grouped",
+    "grouped_linear_forward", "grouped_linear_backward", "MAX_GROUPS", "ROWWISE", "COLWISE_T", "BOTH", "E5M2", "FWD", "DGRAD", "WGRAD", "A_E5M2", "B_E5M2",
     "OUT_F32", "MAX_WEIGHTS", "Fp8BlkError",
     "LIB_PATH", "status_string",
 ]
@@ -352,4 +363,105 @@ def linear_backward(x, w, dy, stream=None):
     _, _, qxT, sxT = fp8blk_quantize_act_1x128(x, COLWISE_T, stream=stream)
     dx = fp8blk_gemm(DGRAD, qdy, sdy, qwT, swT, stream=stream)
     dw = fp8blk_gemm(WGRAD, qdyT, sdyT, qxT, sxT, stream=stream)
+    return dx, dw
+
+
+def fp8blk_grouped_padded_rows(rows: int, groups: int) -> int:
+    """Columns of the COLWISE_T outputs for `rows` rows in `groups` groups (whole 128-token blocks each)."""
+    return int(lib.fp8blk_grouped_padded_rows(int(rows), int(groups)))
+
+
+def _offsets(offsets) -> int:
+    """Checks the offsets of rows sorted by group; returns the number of groups."""
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int32 tensor [groups + 1]")
+    groups = offsets.numel() - 1
+    if not 1 <= groups <= MAX_GROUPS:
+        raise ValueError(f"between 1 and {MAX_GROUPS} groups")
+    return groups
+
+
+def fp8blk_quantize_act_1x128_grouped(x, offsets, mode=ROWWISE, q_row=None, s_row=None, q_colT=None, s_colT=None,
+                                      stream=None):
+    """Activation quantisation in 1x128 groups of rows sorted by group (offsets: int32 [groups + 1] on
+    the device).  Any number of rows; groups of 128 tokens start anew in every group.  Returns (q_row,
+    s_row, q_colT, s_colT); unused are None.  ``mode`` may include E5M2."""
+    x = _bf16_2d(x)
+    groups = _offsets(offsets)
+    dev = _need_cuda(x, offsets, q_row, s_row, q_colT, s_colT)
+    rows, cols = x.shape
+    code_dtype = E5M2_DTYPE if mode & E5M2 else E4M3
+    if mode & ROWWISE:
+        q_row = _out(q_row, (rows, cols), code_dtype, dev)
+        s_row = _out(s_row, (cols // 128, rows), torch.float32, dev)
+    else:
+        q_row = s_row = None
+    if mode & COLWISE_T:
+        padded = fp8blk_grouped_padded_rows(rows, groups)
+        q_colT = _out(q_colT, (cols, padded), code_dtype, dev)
+        s_colT = _out(s_colT, (padded // 128, cols), torch.float32, dev)
+    else:
+        q_colT = s_colT = None
+    _run(dev, lib.fp8blk_quantize_act_1x128_grouped, _ptr(x), rows, cols, max(x.stride(0), cols), int(mode),
+         _ptr(offsets), groups, _ptr(q_row), _ptr(s_row), _ptr(q_colT), _ptr(s_colT), _stream_handle(stream, dev))
+    return q_row, s_row, q_colT, s_colT
+
+
+def fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, d=None, stream=None, out_dtype=torch.bfloat16):
+    """The GEMM of a layer with one weight per group, over rows sorted by group (offsets: int32
+    [groups + 1] on the device).  FWD: Y[T,out] from a[T,in], b[groups*out,in]; DGRAD: dX[T,in] from
+    a[T,out], b[in,groups*out]; WGRAD: dW[groups,out,in] from a[out,P], b[in,P].  bf16, or fp32 with
+    out_dtype=torch.float32 or an fp32 d.  Rows of d outside every group are left as they were."""
+    groups = _offsets(offsets)
+    dev = _need_cuda(a, sa, b, sb, offsets, d)
+    if a.dim() != 2 or b.dim() != 2 or a.dtype not in (E4M3, E5M2_DTYPE) or b.dtype not in (E4M3, E5M2_DTYPE):
+        raise ValueError("A and B must be 2-D float8_e4m3fn or float8_e5m2")
+    m, k = a.shape
+    if layout == WGRAD:
+        n = b.shape[0]
+        want_b, want_sb, shape = (n, k), (k // 128, n), (groups, m, n)
+    elif layout == FWD:
+        n = b.shape[0] // groups
+        want_b, want_sb, shape = (groups * n, k), (groups * n // 128, k // 128), (m, n)
+    elif layout == DGRAD:
+        n = b.shape[0]
+        want_b, want_sb, shape = (n, groups * k), (n // 128, groups * k // 128), (m, n)
+    else:
+        raise ValueError("layout must be FWD, DGRAD or WGRAD")
+    if tuple(b.shape) != want_b:
+        raise ValueError(f"B {tuple(b.shape)} does not match A {tuple(a.shape)} and {groups} groups")
+    if tuple(sa.shape) != (k // 128, m) or tuple(sb.shape) != want_sb:
+        raise ValueError(f"scale shapes {tuple(sa.shape)}, {tuple(sb.shape)} do not match layout {layout}")
+    if sa.dtype != torch.float32 or sb.dtype != torch.float32:
+        raise ValueError("scales must be float32")
+    if not (a.is_contiguous() and b.is_contiguous() and sa.is_contiguous() and sb.is_contiguous()):
+        raise ValueError("operands and scales must be contiguous")
+    if d is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        d = torch.empty(shape, dtype=out_dtype, device=dev)
+    elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != shape or d.stride(-1) != 1 or (
+            layout == WGRAD and groups > 1 and d.stride(0) != m * d.stride(1)):
+        raise ValueError(f"d must be a bfloat16 or float32 {shape} tensor with unit column stride and one row pitch")
+    flags = (A_E5M2 if a.dtype == E5M2_DTYPE else 0) | (B_E5M2 if b.dtype == E5M2_DTYPE else 0)
+    flags |= OUT_F32 if d.dtype == torch.float32 else 0
+    _run(dev, lib.fp8blk_gemm_grouped, int(layout) | flags, groups, _ptr(offsets), m, n, k, _ptr(a), _ptr(sa), _ptr(b),
+         _ptr(sb), _ptr(d), max(d.stride(-2), n), _stream_handle(stream, dev))
+    return d
+
+
+def grouped_linear_forward(x, qw, sw, offsets, stream=None):
+    """Y[t] = X[t] . W[e]^T for the rows t of group e: X quantised here (1x128), W [groups,out,in] ahead, as
+    one weight of groups*out rows (fp8blk_quantize_weight_128x128: qw [groups*out,in], sw)."""
+    qx, sx, _, _ = fp8blk_quantize_act_1x128_grouped(x, offsets, ROWWISE, stream=stream)
+    return fp8blk_gemm_grouped(FWD, qx, sx, qw, sw, offsets, stream=stream)
+
+
+def grouped_linear_backward(x, dy, qwT, swT, offsets, stream=None, out_dtype=torch.bfloat16):
+    """(dX [T,in], dW [groups,out,in]) of grouped_linear_forward, both FP8 blockwise; the transposed weights
+    come quantised (fp8blk_quantize_weight_128x128_t or _both: qwT [in,groups*out], swT).  out_dtype: dW's."""
+    qdy, sdy, qdyT, sdyT = fp8blk_quantize_act_1x128_grouped(dy, offsets, BOTH, stream=stream)
+    _, _, qxT, sxT = fp8blk_quantize_act_1x128_grouped(x, offsets, COLWISE_T, stream=stream)
+    dx = fp8blk_gemm_grouped(DGRAD, qdy, sdy, qwT, swT, offsets, stream=stream)
+    dw = fp8blk_gemm_grouped(WGRAD, qdyT, sdyT, qxT, sxT, offsets, stream=stream, out_dtype=out_dtype)
     return dx, dw

@@ -35,6 +35,7 @@ class WeightDesc(ctypes.Structure):
 
 
 MAX_WEIGHTS = 8   # FP8BLK_MAX_WEIGHTS
+MAX_GROUPS = 1024   # FP8BLK_MAX_GROUPS
 
 
 def _load() -> ctypes.CDLL:
@@ -57,6 +58,9 @@ def _load() -> ctypes.CDLL:
         "fp8blk_quantize_tensor": [P, I64, I64, I64, P, P, P],
         "fp8blk_gemm_tensor_scaled": [I64, I64, I64, P, P, P, P, P, I64, P],
         "fp8blk_gemm": [I, I64, I64, I64, P, P, P, P, P, I64, P],
+        "fp8blk_grouped_padded_rows": [I64, I64],
+        "fp8blk_quantize_act_1x128_grouped": [P, I64, I64, I64, I, P, I64, P, P, P, P, P],
+        "fp8blk_gemm_grouped": [I, I64, P, I64, I64, I64, P, P, P, P, P, I64, P],
         "fp8blk_gemm_splitk": [I, I64, I64, I64, P, P, P, P, P, I64, I, P, I64, P],
         "fp8blk_gemm_splitk_workspace_bytes": [I, I64, I64, I64, I],
         "fp8blk_gemm_splitk_count": [I, I64, I64, I64],
@@ -70,6 +74,7 @@ def _load() -> ctypes.CDLL:
         fn.argtypes = args
         fn.restype = {"fp8blk_status_string": ctypes.c_char_p,
                       "fp8blk_amax_ema_workspace_bytes": ctypes.c_int64,
+                      "fp8blk_grouped_padded_rows": ctypes.c_int64,
                       "fp8blk_gemm_splitk_workspace_bytes": ctypes.c_int64}.get(name, ctypes.c_int)
     return so
 

@@ -7,6 +7,7 @@
 #include "../../include/fp8blk.h"
 #include "context.h"
 #include "device.cuh"
+#include "groups.cuh"
 #include "kernels.h"
 
 namespace fp8blk {
@@ -102,6 +103,25 @@ fp8blk_status check_quant_common(const void* x, int64_t rows, int64_t cols, int6
   return FP8BLK_OK;
 }
 
+// Checks the mode and the outputs of an activation quantisation; fills the kernel mode.
+fp8blk_status act_outputs(int mode, const uint8_t* q_row, const float* s_row, const uint8_t* q_colT,
+                          const float* s_colT, int* kmode) {
+  const int base = mode & ~FP8BLK_E5M2;
+  if (base != FP8BLK_ROWWISE && base != FP8BLK_COLWISE_T && base != FP8BLK_BOTH) return FP8BLK_ERR_INVALID_ARG;
+  *kmode = (mode & FP8BLK_E5M2) ? fp8blk::Q_E5M2 : 0;
+  if (mode & FP8BLK_ROWWISE) {
+    if (!q_row || !s_row) return FP8BLK_ERR_INVALID_ARG;
+    if (!aligned16(q_row) || !aligned16(s_row)) return FP8BLK_ERR_ALIGN;
+    *kmode |= fp8blk::Q_ROW;
+  }
+  if (mode & FP8BLK_COLWISE_T) {
+    if (!q_colT || !s_colT) return FP8BLK_ERR_INVALID_ARG;
+    if (!aligned16(q_colT) || !aligned16(s_colT)) return FP8BLK_ERR_ALIGN;
+    *kmode |= fp8blk::Q_COLT;
+  }
+  return FP8BLK_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,24 +131,45 @@ fp8blk_status fp8blk_quantize_act_1x128(const void* x, int64_t rows, int64_t col
                                         void* stream) {
   fp8blk_status st = check_quant_common(x, rows, cols, ldx);
   if (st != FP8BLK_OK) return st;
-  const int base = mode & ~FP8BLK_E5M2;
-  if (base != FP8BLK_ROWWISE && base != FP8BLK_COLWISE_T && base != FP8BLK_BOTH) return FP8BLK_ERR_INVALID_ARG;
-  int kmode = (mode & FP8BLK_E5M2) ? fp8blk::Q_E5M2 : 0;
-  if (mode & FP8BLK_ROWWISE) {
-    if (!q_row || !s_row) return FP8BLK_ERR_INVALID_ARG;
-    if (!aligned16(q_row) || !aligned16(s_row)) return FP8BLK_ERR_ALIGN;
-    kmode |= fp8blk::Q_ROW;
-  }
-  if (mode & FP8BLK_COLWISE_T) {
-    if (!q_colT || !s_colT) return FP8BLK_ERR_INVALID_ARG;
-    if (!aligned16(q_colT) || !aligned16(s_colT)) return FP8BLK_ERR_ALIGN;
-    kmode |= fp8blk::Q_COLT;
-  }
+  int kmode = 0;
+  if ((st = act_outputs(mode, q_row, s_row, q_colT, s_colT, &kmode)) != FP8BLK_OK) return st;
   if ((st = check_device()) != FP8BLK_OK) return st;
   QuantArgs a{static_cast<const uint16_t*>(x), rows, cols, ldx, q_row, s_row, q_colT, s_colT, rows / 128,
               cols / 128};
   if ((st = set_quant_waits(a)) != FP8BLK_OK) return st;
   return launch_status(fp8blk::launch_quant(kmode, a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t fp8blk_grouped_padded_rows(int64_t rows, int64_t groups) {
+  if (rows < 0 || groups < 1 || groups > FP8BLK_MAX_GROUPS) return -1;
+  return (rows + 127 * (groups < rows ? groups : rows)) / 128 * 128;
+}
+
+fp8blk_status fp8blk_quantize_act_1x128_grouped(const void* x, int64_t rows, int64_t cols, int64_t ldx, int mode,
+                                                const int32_t* offsets, int64_t groups, uint8_t* q_row, float* s_row,
+                                                uint8_t* q_colT, float* s_colT, void* stream) {
+  static_assert(FP8BLK_MAX_GROUPS == fp8blk::kMaxGroups, "the kernels' tables hold every group");
+  if (!offsets || groups < 1 || groups > FP8BLK_MAX_GROUPS) return FP8BLK_ERR_INVALID_ARG;
+  if (rows < 0 || !dim_ok(cols)) return FP8BLK_ERR_SHAPE;
+  const int64_t padded = fp8blk_grouped_padded_rows(rows, groups);
+  // 32-bit tile counts, and 32-bit offsets inside a tile's 128 transposed rows.
+  if (padded > (int64_t(1) << 25) || (padded / 128 + 1) * (cols / 128) >= (int64_t(1) << 31)) return FP8BLK_ERR_SHAPE;
+  if (ldx < cols) return FP8BLK_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(offsets) & 3u) return FP8BLK_ERR_ALIGN;
+  if (rows == 0) return (mode & ~(FP8BLK_BOTH | FP8BLK_E5M2)) || !(mode & FP8BLK_BOTH) ? FP8BLK_ERR_INVALID_ARG : FP8BLK_OK;
+  if (!x) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(x) || ldx % 8 != 0) return FP8BLK_ERR_ALIGN;
+  int kmode = 0;
+  fp8blk_status st = act_outputs(mode, q_row, s_row, q_colT, s_colT, &kmode);
+  if (st != FP8BLK_OK) return st;
+  if ((st = check_device()) != FP8BLK_OK) return st;
+  QuantArgs a{static_cast<const uint16_t*>(x), rows, cols, ldx, q_row, s_row, q_colT, s_colT, padded / 128,
+              cols / 128};
+  if ((st = set_quant_waits(a)) != FP8BLK_OK) return st;
+  a.offsets = offsets;
+  a.groups = static_cast<int>(groups);
+  a.padded_rows = padded;
+  return launch_status(fp8blk::launch_quant_grouped(kmode, a, static_cast<cudaStream_t>(stream)));
 }
 
 // Checks of one weight quantisation in 128x128 blocks: (q, s) in place and/or
@@ -258,6 +299,64 @@ fp8blk_status fp8blk_gemm(int layout, int64_t M, int64_t N, int64_t K, const uin
   const fp8blk_status st = gemm_args(layout, M, N, K, a, sa, b, sb, d, ldd, g);
   if (st != FP8BLK_OK) return st;
   return launch_status(fp8blk::launch_gemm(g, static_cast<cudaStream_t>(stream)));
+}
+
+fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                                  const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, void* d,
+                                  int64_t ldd, void* stream) {
+  const int formats = layout & (FP8BLK_A_E5M2 | FP8BLK_B_E5M2);
+  const bool out_f32 = (layout & FP8BLK_OUT_F32) != 0;
+  layout &= ~(FP8BLK_A_E5M2 | FP8BLK_B_E5M2 | FP8BLK_OUT_F32);
+  if (layout != FP8BLK_FWD && layout != FP8BLK_DGRAD && layout != FP8BLK_WGRAD) return FP8BLK_ERR_INVALID_ARG;
+  if (!offsets || groups < 1 || groups > FP8BLK_MAX_GROUPS) return FP8BLK_ERR_INVALID_ARG;
+  const bool wgrad = layout == FP8BLK_WGRAD;
+  // Ragged: the rows (FWD / DGRAD: M, any number; WGRAD: K, whole 128-token blocks, maybe none).
+  if (!dim_ok(N) || (wgrad ? !dim_ok(M) || K < 0 || K % 128 : M < 0 || !dim_ok(K))) return FP8BLK_ERR_SHAPE;
+  // 32-bit TMA coordinates and tile counts.
+  constexpr int64_t kMost = int64_t(1) << 31;
+  const int64_t rows = wgrad ? K : M;
+  const int64_t blocks = wgrad ? groups * (M / 128) : M / 128 + groups;
+  if (rows >= kMost - 128 || groups * N >= kMost || (wgrad ? groups * M : groups * K) >= kMost ||
+      blocks * (N / 128) >= kMost - 1024)
+    return FP8BLK_ERR_SHAPE;
+  if (ldd < N) return FP8BLK_ERR_INVALID_ARG;
+  if (!wgrad && M == 0) return FP8BLK_OK;
+  if (!b || !sb || !d || (rows != 0 && (!a || !sa))) {
+    if (!d || !(wgrad && rows == 0)) return FP8BLK_ERR_INVALID_ARG;   // WGRAD of no rows writes zeros
+  }
+  if (!aligned16(a) || !aligned16(b) || (reinterpret_cast<uintptr_t>(d) & 31u) || ldd % (out_f32 ? 8 : 16) != 0)
+    return FP8BLK_ERR_ALIGN;
+  // WGRAD's scales and the per-block scales; FWD and DGRAD read sa by single words.
+  if (!aligned16(sa) || !aligned16(sb) || (reinterpret_cast<uintptr_t>(offsets) & 3u)) return FP8BLK_ERR_ALIGN;
+  fp8blk_status st = check_device();
+  if (st != FP8BLK_OK) return st;
+  fp8blk::GroupedGemmArgs g{};
+  g.layout = layout;
+  g.groups = groups;
+  g.offsets = offsets;
+  g.rows = rows;
+  g.padded_rows = wgrad ? K : 0;
+  g.m = wgrad ? M : 0;
+  g.n = N;
+  g.k = wgrad ? 0 : K;
+  g.a = a;
+  g.sa = sa;
+  g.b = b;
+  g.sb = sb;
+  g.d = d;
+  g.ldd = ldd;
+  g.out_f32 = out_f32;
+  g.timeout_ns = wait_timeout_ns();
+  g.err = error_word();
+  if (!g.err) return FP8BLK_ERR_CUDA;
+  g.pdl = pdl_enabled();
+  g.a_e5m2 = (formats & FP8BLK_A_E5M2) != 0;
+  g.b_e5m2 = (formats & FP8BLK_B_E5M2) != 0;
+  g.max_ctas = env_int("FP8BLK_GEMM_MAX_CTAS", 0);
+  g.group_m = env_int("FP8BLK_GEMM_GROUP_M", 0);
+  g.block_n = env_int("FP8BLK_GEMM_BLOCK_N", 0);
+  g.inject_stall = env_int("FP8BLK_TEST_INJECT_STALL", 0) != 0;
+  return launch_status(fp8blk::launch_gemm_grouped(g, static_cast<cudaStream_t>(stream)));
 }
 
 int fp8blk_gemm_splitk_count(int layout, int64_t M, int64_t N, int64_t K) {

@@ -24,9 +24,15 @@ struct QuantArgs {
   unsigned int* err;     // device error word
   int pdl;               // 1 = launch with programmatic stream serialization
   int max_ctas;          // > 0: at most this many CTAs (leaves SMs to concurrent work)
+  const int* offsets;    // ragged launch: row ranges of the groups, groups + 1 device words
+  int groups;            // (tiles_r is then an upper bound)
+  int64_t padded_rows;   // pitch of q_t and 128 times the rows of s_t
 };
 
 cudaError_t launch_quant(int mode, const QuantArgs& a, cudaStream_t stream);
+
+// The activation modes over rows sorted by group (see groups.cuh).
+cudaError_t launch_quant_grouped(int mode, const QuantArgs& a, cudaStream_t stream);
 
 // The weight quantiser (both 128x128 block layouts) over up to kQuantMaxGroup
 // tensors in one launch; w[0] also carries the launch-wide fields (waits,
@@ -99,6 +105,34 @@ int choose_splits(const GemmArgs& g);
 // device (tile width and SM count as the launch will use them).
 int64_t splitk_workspace_bytes(const GemmArgs& g);
 
+// GEMMs with one weight per group over rows sorted by group (gemm_grouped.cu).
+struct GroupedGemmArgs {
+  int layout;                 // 0 FWD, 1 DGRAD, 2 WGRAD
+  int64_t groups;
+  const int* offsets;         // device, groups + 1
+  int64_t rows;               // T
+  int64_t padded_rows;        // WGRAD: columns of a and b
+  int64_t m;                  // WGRAD: output rows of each group
+  int64_t n;                  // output columns
+  int64_t k;                  // FWD / DGRAD: contraction
+  const uint8_t* a;           // [T][k];  WGRAD [m][padded_rows]
+  const float* sa;            // [k/128][T];  WGRAD [padded_rows/128][m]
+  const uint8_t* b;           // FWD [groups * n][k], DGRAD [n][groups * k], WGRAD [n][padded_rows]
+  const float* sb;            // FWD [groups * n/128][k/128], DGRAD [n/128][groups * k/128], WGRAD [padded_rows/128][n]
+  void* d;                    // [T][ldd];  WGRAD [groups * m][ldd]
+  int64_t ldd;
+  int out_f32;
+  uint64_t timeout_ns;
+  int inject_stall;
+  int block_n;                // 128: narrow tiles, else 256 where n allows them
+  int group_m;
+  int pdl;
+  int max_ctas;
+  int a_e5m2, b_e5m2;
+  unsigned int* err;
+};
+
+cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, cudaStream_t stream);
 
 // y[i] = bf16_round_nearest_even(x[i]) for i < n (x, y 16-byte aligned).
 cudaError_t launch_round_bf16(const float* x, int64_t n, uint16_t* y, int pdl, cudaStream_t stream);

@@ -39,12 +39,22 @@
 // gives -0 -> 0x80 and +0 -> 0x00.  No branch, no data-dependent cost.  The
 // saturating conversion equals clamp-then-round because every value above
 // 448 rounds or saturates to 448.
+//
+// The ragged variant (kRagged) serves rows sorted by group (a layer's tokens
+// sorted by expert): its row tiles start anew at every group's first row, so
+// that no group of 128 tokens straddles two experts, and rows of the tile
+// behind the group's last one count as zeros.  In-place codes keep the ragged
+// rows; the transposed codes and their scales give every group whole 128-token
+// blocks, one after the other, the last one padded with zero codes.  The
+// number of tiles is known on the device only: every CTA builds the groups'
+// block counts from the offsets (one warp, a scan) before its first load.
 #include <cuda_fp8.h>
 
 #include <cstring>
 
 #include "context.h"
 #include "device.cuh"
+#include "groups.cuh"
 #include "kernels.h"
 #include "qmath.cuh"
 
@@ -68,7 +78,8 @@ struct QCtrl {
   uint64_t full[3], empty[3];
   uint64_t never;            // completed by nothing: the stall test waits on it
   int abort;
-  uint32_t coord[3][3];      // tensor table launches: (tensor, row tile, column tile) of each stage
+  uint32_t coord[3][4];      // of each stage: (tensor, row tile, column tile) of a table launch, (first row, rows,
+                             // column tile, row block) of a ragged one
   float warpmax[2][8];                   // per-warp block maxima, double-buffered by tile parity
   alignas(16) float2 qs[kTile];          // per-column {s, -1/s}
   alignas(16) float4 rq[8][2][4];        // per half-warp, row pair p: {s_2p, s_2p+1, -1/s_2p, -1/s_2p+1}
@@ -77,9 +88,9 @@ struct QCtrl {
 static_assert(sizeof(QCtrl) % 16 == 0, "QCtrl keeps 16-byte alignment");
 constexpr int kCsBytes = kTile * kTile;           // transposed codes, 128-byte rows, 16-B chunks swizzled
 
-template <int MODE>
+template <int MODE, bool kRagged = false>
 __host__ __device__ constexpr int smem_bytes_for() {
-  return stages_for<MODE>() * static_cast<int>(kTileBytes) + ((MODE & (Q_COLT | Q_BLKT)) ? kCsBytes : 0) +
+  return (kRagged ? kMaxGroups * 4 : 0) + stages_for<MODE>() * static_cast<int>(kTileBytes) + ((MODE & (Q_COLT | Q_BLKT)) ? kCsBytes : 0) +
          static_cast<int>(sizeof(QCtrl)) + 1024;  // + alignment slack for the 1024-byte aligned base
 }
 
@@ -116,8 +127,9 @@ __device__ __forceinline__ bool consumers_all(bool v) {
 // launch): their tiles are numbered one tensor after the other, L.tile_end[g]
 // being the tiles of tensors 0 .. g together.  With N > 1 thread 0 publishes
 // each stage's (tensor, row tile, column tile) with the stage, since the
-// consumers cannot step through the tensor boundaries on their own.
-template <int MODE, int N>
+// consumers cannot step through the tensor boundaries on their own; the ragged
+// variant does the same with a tile's first row, row count and block.
+template <int MODE, int N, bool kRagged = false>
 __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_constant__ QuantLaunch<N> L) {
   constexpr bool kRow = MODE & Q_ROW;
   constexpr bool kColT = MODE & Q_COLT;
@@ -132,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* cs = smem + S * kTileBytes;                                      // [128][128 B] (transposed paths)
   QCtrl* ctrl = reinterpret_cast<QCtrl*>(cs + (kTileSmem ? kCsBytes : 0));
+  [[maybe_unused]] int* block_ends = reinterpret_cast<int*>(ctrl + 1);       // kRagged: blocks of groups 0 .. e
 
   const int t = threadIdx.x;
   const int lane = t & 31, warp = t >> 5;
@@ -140,8 +153,25 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
   // of its tensor; with one tensor a CTA's tiles are gridDim.x apart, so their
   // coordinates advance by fixed steps (32-bit: the host rejects 2^31 tiles
   // or more).
-  const uint32_t tiles_r = static_cast<uint32_t>(a0.tiles_r);
-  const uint32_t tiles = L.tile_end[N - 1];
+  uint32_t tiles_r = static_cast<uint32_t>(a0.tiles_r);
+  uint32_t tiles = L.tile_end[N - 1];
+  [[maybe_unused]] int first_row = 0, end_row = 0;   // kRagged, in place only: the rows of all groups
+  if constexpr (kRagged) {
+    griddep_wait();                              // the offsets may come from the previous kernel
+    const int rows = static_cast<int>(a0.rows);
+    if constexpr (kColT) {
+      if (warp == 0) build_block_ends(block_ends, a0.offsets, a0.groups, rows, lane);
+      __syncthreads();
+      tiles_r = min(static_cast<uint32_t>(block_ends[a0.groups - 1]),
+                    static_cast<uint32_t>(a0.padded_rows / kTile));
+    } else {
+      first_row = clamp_row(__ldg(a0.offsets), rows);
+      end_row = clamp_row(__ldg(a0.offsets + a0.groups), rows);
+      tiles_r = static_cast<uint32_t>(max(end_row - first_row, 0) + kTile - 1) / kTile;
+    }
+    tiles = tiles_r * static_cast<uint32_t>(a0.tiles_c);
+    if (tiles == 0) return;                      // no rows at all (the whole block leaves)
+  }
   const uint32_t step_r = gridDim.x % tiles_r, step_c = gridDim.x / tiles_r;
   auto advance = [&](uint32_t& tr, uint32_t& tc) {
     tr += step_r;
@@ -152,9 +182,32 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
     }
   };
   // Loads tile j into `stage`; (ltr, ltc) are its coordinates when N == 1.
-  uint32_t lg = 0;                                                   // tensor of the next load (N > 1)
+  uint32_t lg = 0;                                                   // tensor (N > 1) or group of the last load
+  [[maybe_unused]] uint32_t lblock = 0;                              // kRagged: row block of the last load
   auto load_tile = [&](int stage, uint32_t j, uint32_t ltr, uint32_t ltc) {
     uint32_t g = 0, tr = ltr, tc = ltc;
+    if constexpr (kRagged) {
+      int row0, valid;
+      if constexpr (kColT) {
+        lg = static_cast<uint32_t>(find_group(block_ends, a0.groups, static_cast<int>(tr),
+                                              tr >= lblock ? static_cast<int>(lg) : 0));
+        lblock = tr;
+        int size;
+        const int local = static_cast<int>(tr) - (lg ? block_ends[lg - 1] : 0);
+        row0 = group_rows(a0.offsets, static_cast<int>(lg), static_cast<int>(a0.rows), &size) + local * kTile;
+        valid = min(size - local * kTile, kTile);
+      } else {
+        row0 = first_row + static_cast<int>(tr) * kTile;
+        valid = min(end_row - row0, kTile);
+      }
+      ctrl->coord[stage][0] = static_cast<uint32_t>(row0);
+      ctrl->coord[stage][1] = static_cast<uint32_t>(valid);
+      ctrl->coord[stage][2] = tc;
+      ctrl->coord[stage][3] = tr;
+      mbar_arrive_expect_tx(&ctrl->full[stage], kTileBytes);   // rows behind the tensor arrive as zeros
+      tma_load_2d(smem + stage * kTileBytes, &L.map[0], &ctrl->full[stage], static_cast<int>(tc * kTile), row0);
+      return;
+    }
     if constexpr (N > 1) {
       while (j >= L.tile_end[lg]) ++lg;          // a CTA's tiles only move forward
       g = lg;
@@ -220,17 +273,34 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
         tc = ctrl->coord[s][2];
       }
     }
+    [[maybe_unused]] int64_t ragged_row0 = 0;
+    [[maybe_unused]] int valid = kTile;          // kRagged: rows of the tile that belong to its group
+    if constexpr (kRagged) {
+      if (ok) {
+        ragged_row0 = static_cast<int64_t>(ctrl->coord[s][0]);
+        valid = static_cast<int>(ctrl->coord[s][1]);
+        tc = ctrl->coord[s][2];
+        tr = ctrl->coord[s][3];
+      }
+    }
     if (!consumers_all(ok)) break;
     const QuantArgs& a = L.t[g];
     const uint32_t cols = static_cast<uint32_t>(a.cols);
-    const uint32_t rows = static_cast<uint32_t>(a.rows);
+    // Pitch of the transposed codes: the tensor's rows, or the groups' padded ones.
+    const uint32_t rows = static_cast<uint32_t>(kRagged ? a.padded_rows : a.rows);
 
-    const int64_t row0 = static_cast<int64_t>(tr) * kTile, col0 = static_cast<int64_t>(tc) * kTile;
+    const int64_t row0 = kRagged ? ragged_row0 : static_cast<int64_t>(tr) * kTile;
+    const int64_t col0 = static_cast<int64_t>(tc) * kTile;
     uint4 v[8];
     {
       const uint8_t* xs = smem + s * kTileBytes + (8 * bi) * 256 + bj * 16;   // conflict-free: 2 rows per warp
 #pragma unroll
       for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const uint4*>(xs + r * 256);
+    }
+    if constexpr (kRagged && kColT) {            // another group's rows
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (8 * bi + r >= valid) v[r] = make_uint4(0, 0, 0, 0);
     }
     __syncwarp();                                // everything else comes from registers: hand the stage back
     if (lane == 0) mbar_arrive(&ctrl->empty[s]);
@@ -292,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
         float* rp = reinterpret_cast<float*>(&rq[rho >> 1]);
         rp[rho & 1] = q.s;
         rp[2 + (rho & 1)] = q.nr;
-        a.s_row[static_cast<int64_t>(tc) * a.rows + row0 + 8 * bi + rho] = q.s;
+        if (!kRagged || 8 * bi + rho < valid) a.s_row[static_cast<int64_t>(tc) * a.rows + row0 + 8 * bi + rho] = q.s;
       }
       __syncwarp();
     }
@@ -375,10 +445,10 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
         float2 w[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) w[c] = neg_quotient2(x[c], s2, nr2);
-        *reinterpret_cast<uint2*>(qdst + (2 * p) * cols) =
+        if (!kRagged || 8 * bi + 2 * p < valid) *reinterpret_cast<uint2*>(qdst + (2 * p) * cols) =
             make_uint2(cvt4<kE5>(w[0].x, w[1].x, w[2].x, w[3].x) ^ 0x80808080u,
                        cvt4<kE5>(w[4].x, w[5].x, w[6].x, w[7].x) ^ 0x80808080u);
-        *reinterpret_cast<uint2*>(qdst + (2 * p + 1) * cols) =
+        if (!kRagged || 8 * bi + 2 * p + 1 < valid) *reinterpret_cast<uint2*>(qdst + (2 * p + 1) * cols) =
             make_uint2(cvt4<kE5>(w[0].y, w[1].y, w[2].y, w[3].y) ^ 0x80808080u,
                        cvt4<kE5>(w[4].y, w[5].y, w[6].y, w[7].y) ^ 0x80808080u);
       }
@@ -403,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
       // Column cc's logical 16-byte part m (tokens 16 m .. 16 m + 15) holds units
       // 2m and 2m + 1, stored at units (2m) ^ x and (2m + 1) ^ x, x = cc / 8: the
       // same 16-byte chunk m ^ (x / 2), halves swapped when x is odd.
-      uint8_t* tdst = a.q_t + col0 * a.rows + row0;
+      uint8_t* tdst = kRagged ? a.q_t + col0 * a.padded_rows + static_cast<int64_t>(tr) * kTile : a.q_t + col0 * a.rows + row0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int k = t + kConsumers * j;
@@ -442,19 +512,19 @@ bool make_input_map(CUtensorMap* map, const QuantArgs& a) {
 
 // Launches quant_tile_kernel<MODE, N> over the tensors a[0 .. count-1]
 // (count <= N; the table's unused entries repeat the last tile count).
-template <int MODE, int N>
+template <int MODE, int N, bool kRagged = false>
 cudaError_t launch_mode(const QuantArgs* a, int count, cudaStream_t stream) {
   static PerContext<int> resident;   // resident CTAs on the device, after the shared-memory opt-in
-  constexpr int kSmem = smem_bytes_for<MODE>();
+  constexpr int kSmem = smem_bytes_for<MODE, kRagged>();
   int grid_cap = 0;
   cudaError_t e = resident.get(&grid_cap, [](int* cap) {
     cudaError_t r =
-        cudaFuncSetAttribute(quant_tile_kernel<MODE, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaFuncSetAttribute(quant_tile_kernel<MODE, N, kRagged>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     int dev = 0, sms = 0, per_sm = 0;
     if (r == cudaSuccess) r = cudaGetDevice(&dev);
     if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (r == cudaSuccess)
-      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, quant_tile_kernel<MODE, N>, kThreads, kSmem);
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, quant_tile_kernel<MODE, N, kRagged>, kThreads, kSmem);
     *cap = sms * (per_sm > 0 ? per_sm : 1);
     return r;
   });
@@ -485,7 +555,7 @@ cudaError_t launch_mode(const QuantArgs* a, int count, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   cfg.numAttrs = set_pdl_attr(attr, a[0].pdl);
   cfg.attrs = attr;
-  e = cudaLaunchKernelEx(&cfg, quant_tile_kernel<MODE, N>, L);
+  e = cudaLaunchKernelEx(&cfg, quant_tile_kernel<MODE, N, kRagged>, L);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -503,6 +573,18 @@ cudaError_t launch_quant(int mode, const QuantArgs& a, cudaStream_t stream) {
     case Q_ROW | Q_E5M2: return launch_mode<Q_ROW | Q_E5M2, 1>(&a, 1, stream);
     case Q_COLT | Q_E5M2: return launch_mode<Q_COLT | Q_E5M2, 1>(&a, 1, stream);
     case Q_ROW | Q_COLT | Q_E5M2: return launch_mode<Q_ROW | Q_COLT | Q_E5M2, 1>(&a, 1, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_quant_grouped(int mode, const QuantArgs& a, cudaStream_t stream) {
+  switch (mode) {
+    case Q_ROW: return launch_mode<Q_ROW, 1, true>(&a, 1, stream);
+    case Q_COLT: return launch_mode<Q_COLT, 1, true>(&a, 1, stream);
+    case Q_ROW | Q_COLT: return launch_mode<Q_ROW | Q_COLT, 1, true>(&a, 1, stream);
+    case Q_ROW | Q_E5M2: return launch_mode<Q_ROW | Q_E5M2, 1, true>(&a, 1, stream);
+    case Q_COLT | Q_E5M2: return launch_mode<Q_COLT | Q_E5M2, 1, true>(&a, 1, stream);
+    case Q_ROW | Q_COLT | Q_E5M2: return launch_mode<Q_ROW | Q_COLT | Q_E5M2, 1, true>(&a, 1, stream);
     default: return cudaErrorInvalidValue;
   }
 }

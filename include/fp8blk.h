@@ -21,7 +21,8 @@
  *  - Matrices are row-major; "[R][C]" means C contiguous elements per row.
  *    bf16 inputs are raw bfloat16 bit patterns (uint16).  E4M3 codes are
  *    float8_e4m3fn bytes.  Scales are IEEE binary32.
- *  - Every dimension must be a positive multiple of 128 (FP8BLK_ERR_SHAPE).
+ *  - Every dimension must be a positive multiple of 128 (FP8BLK_ERR_SHAPE),
+ *    except where an entry point says otherwise (rows sorted by group).
  *    Pointers must be 16-byte aligned and leading dimensions must give
  *    16-byte aligned rows (FP8BLK_ERR_ALIGN).
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
@@ -124,6 +125,40 @@ fp8blk_status fp8blk_quantize_act_1x128(const void* x, int64_t rows, int64_t col
                                         uint8_t* q_colT, float* s_colT, void* stream);
 
 /*
+ * The same quantisation for rows sorted by group: the tokens of a layer with
+ * one weight per group (expert), sorted by expert.  Group e owns rows
+ * offsets[e] .. offsets[e + 1] - 1; any of them may be empty.
+ *
+ *   x        [rows][ldx] bf16, rows >= 0 (any number), cols a multiple of 128.
+ *   offsets  DEVICE int32 [groups + 1], not decreasing, offsets[0] >= 0,
+ *            offsets[groups] <= rows.  Rows outside every group are not read
+ *            into any result, and their codes and scales are left as they
+ *            were.  The array is read on the device: one that breaks these
+ *            rules gives unspecified codes, but no access out of range.
+ *   groups   1 .. FP8BLK_MAX_GROUPS.
+ *   mode     as above, E5M2 included.
+ *   ROWWISE outputs: q_row [rows][cols], s_row [cols/128][rows], as above (a
+ *            row's groups of 128 columns do not depend on `offsets`).
+ *   COLWISE_T outputs: groups of 128 tokens start anew in every group, the
+ *            last one of a group padded with zero codes to 128.  The blocks of
+ *            all groups stand one after the other:
+ *              q_colT [cols][P], s_colT [P/128][cols],
+ *            P = fp8blk_grouped_padded_rows(rows, groups); group e starts at
+ *            column 128 * sum over i < e of ceil((offsets[i+1] - offsets[i]) / 128).
+ *            What lies behind the last group's last block is left as it was.
+ * FP8BLK_ERR_SHAPE for rows so many that P > 2^25; other errors as above.
+ */
+#define FP8BLK_MAX_GROUPS 1024
+fp8blk_status fp8blk_quantize_act_1x128_grouped(const void* x, int64_t rows, int64_t cols, int64_t ldx, int mode,
+                                                const int32_t* offsets, int64_t groups, uint8_t* q_row, float* s_row,
+                                                uint8_t* q_colT, float* s_colT, void* stream);
+
+/* Columns of the padded layout for any split of `rows` rows into `groups` groups:
+ * (rows + 127 min(groups, rows)) rounded down to a multiple of 128; -1 for
+ * rows < 0 or groups out of range. */
+int64_t fp8blk_grouped_padded_rows(int64_t rows, int64_t groups);
+
+/*
  * Weight quantisation, 128x128 blocks ([DIGEST] "权重 2D 128x128").
  *   w  [n][ldw] bf16 (first k columns used)  ->  q [n][k] E4M3,  s [n/128][k/128] fp32.
  * The forward GEMM takes (q, s) as operand B.
@@ -207,6 +242,39 @@ fp8blk_status fp8blk_quantize_weights_128x128_both(const fp8blk_weight_128x128* 
 fp8blk_status fp8blk_gemm(int layout, int64_t M, int64_t N, int64_t K,
                           const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
                           void* d, int64_t ldd, void* stream);
+
+/*
+ * The GEMMs of a layer with one weight per group (expert), rows sorted by
+ * group as in fp8blk_quantize_act_1x128_grouped (offsets: DEVICE int32
+ * [groups + 1]).  Operands, scales, formats (FP8BLK_A_E5M2, FP8BLK_B_E5M2,
+ * FP8BLK_OUT_F32) and rounding as in fp8blk_gemm; with W [groups][out][in]
+ * quantised as ONE weight of groups * out rows:
+ *
+ *   FWD   : M = rows T (any number), N = out, K = in
+ *           a = X rowwise [T][in],            sa [in/128][T]
+ *           b = q [groups * out][in],         sb [groups * out/128][in/128]
+ *           d = Y [T][ldd],  Y[t] = X[t] . W[e]^T for t in group e
+ *   DGRAD : M = T, N = in, K = out
+ *           a = dY rowwise [T][out],          sa [out/128][T]
+ *           b = qT [in][groups * out],        sb = sT [in/128][groups * out/128]
+ *           d = dX [T][ldd], dX[t] = dY[t] . W[e]
+ *   WGRAD : M = out, N = in, K = P (the padded rows of the COLWISE_T outputs)
+ *           a = dY colwise_T [out][P],        sa [P/128][out]
+ *           b = X colwise_T [in][P],          sb [P/128][in]
+ *           d = dW [groups][out][ldd] (group e at d + e * out * ldd),
+ *           dW[e] = dY_e^T . X_e; zeros for a group without rows
+ *
+ * N, K (FWD / DGRAD) and M (WGRAD) are multiples of 128.  Rows of d outside
+ * every group are left as they were.  Every output element is a fixed sum:
+ * the result does not depend on the other groups' sizes.
+ * Errors as fp8blk_gemm; FP8BLK_ERR_INVALID_ARG for groups out of range or a
+ * null offsets; FP8BLK_ERR_SHAPE also where groups times a dimension, or the
+ * number of output tiles, reaches 2^31.  T == 0 (P == 0) is allowed: nothing
+ * is written (zeros are).
+ */
+fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                                  const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, void* d,
+                                  int64_t ldd, void* stream);
 
 /*
  * The same GEMM with split-K, for shapes whose output tiles leave SMs idle:
