@@ -29,6 +29,13 @@ number of rows in a group):
       FWD  : a[T,in],  b = q[groups*out,in]            -> Y[T,out]
       DGRAD: a[T,out], b = qT[in,groups*out]           -> dX[T,in]
       WGRAD: a[out,P], b[in,P]                         -> dW[groups,out,in]
+
+4-bit microscaled formats (MXFP4, NVFP4; codes and scales as uint8, two codes to a byte):
+  fp8blk_quantize_mx4(x[R,C], fmt, mode)
+      ROWWISE   -> q_row[R,C/2],  s_row[ceil(R/128), ceil(C/(4 block)), 512]
+      COLWISE_T -> q_colT[C,P/2], s_colT for [C,P], P = R rounded up to a multiple of 32
+  fp8blk_dequantize_mx4(q, s, fmt) -> bf16 values
+  fp8blk_gemm_mx4(a[M,K/2], sa, b[N,K/2], sb, fmt) -> d[M,N]
 """
 from __future__ import annotations
 
@@ -36,7 +43,8 @@ import ctypes
 
 import torch
 
-from ._lib import (A_E5M2, B_E5M2, BOTH, COLWISE_T, DGRAD, E5M2, FWD, MAX_GROUPS, MAX_WEIGHTS, OUT_F32, ROWWISE, WGRAD,
+from ._lib import (A_E5M2, B_E5M2, BOTH, COLWISE_T, DGRAD, E5M2, FWD, MAX_GROUPS, MAX_WEIGHTS, MXFP4, NVFP4, OUT_F32, ROWWISE,
+                   WGRAD,
                    Fp8BlkError, LIB_PATH, WeightDesc, check, lib, status_string)
 
 __all__ = [
@@ -46,7 +54,9 @@ __all__ = [
     "fp8blk_quantize_tensor", "fp8blk_gemm_tensor_scaled", "fp8_linear_delayed_forward",
     "fp8blk_gemm", "fp8blk_gemm_splitk", "fp8blk_gemm_splitk_count", "fp8blk_gemm_splitk_workspace_bytes", "fp8blk_round_f32_to_bf16", "fp8blk_get_device_error", "fp8blk_version", "linear_forward",
     "linear_backward", "fp8blk_grouped_padded_rows", "fp8blk_quantize_act_1x128_grouped", "fp8blk_gemm_grouped",
-    "grouped_linear_forward", "grouped_linear_backward", "MAX_GROUPS", "ROWWISE", "COLWISE_T", "BOTH", "E5M2", "FWD", "DGRAD", "WGRAD", "A_E5M2", "B_E5M2",
+    "grouped_linear_forward", "grouped_linear_backward", "MAX_GROUPS", "fp8blk_mx4_scale_bytes", "fp8blk_quantize_mx4",
+    "fp8blk_dequantize_mx4", "fp8blk_gemm_mx4", "mx4_linear_forward", "mx4_linear_wgrad", "mx4_linear_backward",
+    "MXFP4", "NVFP4", "ROWWISE", "COLWISE_T", "BOTH", "E5M2", "FWD", "DGRAD", "WGRAD", "A_E5M2", "B_E5M2",
     "OUT_F32", "MAX_WEIGHTS", "Fp8BlkError",
     "LIB_PATH", "status_string",
 ]
@@ -464,4 +474,124 @@ def grouped_linear_backward(x, dy, qwT, swT, offsets, stream=None, out_dtype=tor
     _, _, qxT, sxT = fp8blk_quantize_act_1x128_grouped(x, offsets, COLWISE_T, stream=stream)
     dx = fp8blk_gemm_grouped(DGRAD, qdy, sdy, qwT, swT, offsets, stream=stream)
     dw = fp8blk_gemm_grouped(WGRAD, qdyT, sdyT, qxT, sxT, offsets, stream=stream, out_dtype=out_dtype)
+    return dx, dw
+
+
+MX4_BLOCK = {MXFP4: 32, NVFP4: 16}
+
+
+def fp8blk_mx4_scale_bytes(fmt, rows: int, k: int) -> int:
+    """Bytes of the scales of a [rows, k] operand in a 4-bit format."""
+    return int(lib.fp8blk_mx4_scale_bytes(int(fmt), int(rows), int(k)))
+
+
+def _mx4_scale_shape(fmt, rows: int, k: int) -> tuple:
+    return -(-rows // 128), -(-k // (4 * MX4_BLOCK[fmt])), 512
+
+
+def _tensor_scale(t):
+    if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+        raise ValueError("a tensor scale is a float32 tensor with one element")
+    return t
+
+
+def _mx4_operand(q, s, fmt, name) -> tuple:
+    """(rows, k) of a 4-bit operand."""
+    if q.dtype != torch.uint8 or q.dim() != 2 or s.dtype != torch.uint8:
+        raise ValueError(f"{name}: codes [rows, k/2] and scales are uint8")
+    rows, k = q.shape[0], 2 * q.shape[1]
+    if tuple(s.shape) != _mx4_scale_shape(fmt, rows, k):
+        raise ValueError(f"{name}: scales must have shape {_mx4_scale_shape(fmt, rows, k)}")
+    if not (q.is_contiguous() and s.is_contiguous()):
+        raise ValueError(f"{name}: codes and scales must be contiguous")
+    return rows, k
+
+
+def fp8blk_quantize_mx4(x, fmt, mode=ROWWISE, tensor_scale=None, q_row=None, s_row=None, q_colT=None, s_colT=None,
+                        stream=None):
+    """4-bit quantisation of a [R,C] bf16 tensor.  fmt: MXFP4 or NVFP4 (tensor_scale: float32 [1] on the
+    device).  Returns (q_row, s_row, q_colT, s_colT); unused are None."""
+    x = _bf16_2d(x)
+    if fmt not in MX4_BLOCK:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    dev = _need_cuda(x, _tensor_scale(tensor_scale), q_row, s_row, q_colT, s_colT)
+    rows, cols = x.shape
+    if mode & ROWWISE:
+        q_row = _out(q_row, (rows, cols // 2), torch.uint8, dev)
+        s_row = _out(s_row, _mx4_scale_shape(fmt, rows, cols), torch.uint8, dev)
+    else:
+        q_row = s_row = None
+    if mode & COLWISE_T:
+        padded = -(-rows // 32) * 32
+        q_colT = _out(q_colT, (cols, padded // 2), torch.uint8, dev)
+        s_colT = _out(s_colT, _mx4_scale_shape(fmt, cols, padded), torch.uint8, dev)
+    else:
+        q_colT = s_colT = None
+    _run(dev, lib.fp8blk_quantize_mx4, _ptr(x), rows, cols, max(x.stride(0), cols) if rows == 1 else x.stride(0),
+         int(mode), int(fmt), _ptr(tensor_scale), _ptr(q_row), _ptr(s_row), _ptr(q_colT), _ptr(s_colT),
+         _stream_handle(stream, dev))
+    return q_row, s_row, q_colT, s_colT
+
+
+def fp8blk_dequantize_mx4(q, s, fmt, tensor_scale=None, y=None, stream=None):
+    """The bf16 values [R,C] of codes q [R,C/2] and scales s of fp8blk_quantize_mx4."""
+    if fmt not in MX4_BLOCK:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    dev = _need_cuda(q, s, _tensor_scale(tensor_scale), y)
+    rows, cols = _mx4_operand(q, s, fmt, "q")
+    if y is None:
+        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    elif y.dtype != torch.bfloat16 or tuple(y.shape) != (rows, cols) or y.stride(1) != 1:
+        raise ValueError(f"y must be a bfloat16 tensor of shape {(rows, cols)} with unit column stride")
+    _run(dev, lib.fp8blk_dequantize_mx4, _ptr(q), _ptr(s), rows, cols, int(fmt), _ptr(tensor_scale), _ptr(y),
+         max(y.stride(0), cols), _stream_handle(stream, dev))
+    return y
+
+
+def fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa=None, tensor_sb=None, d=None, stream=None, out_dtype=torch.bfloat16):
+    """D[M,N] of 4-bit operands a [M,K/2] and b [N,K/2] (fp8blk_quantize_mx4), accumulated in fp32; bf16, or
+    fp32 with out_dtype=torch.float32 or an fp32 d.  A d made here has rows of a multiple of 8 elements."""
+    if fmt not in MX4_BLOCK:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    dev = _need_cuda(a, sa, b, sb, _tensor_scale(tensor_sa), _tensor_scale(tensor_sb), d)
+    m, k = _mx4_operand(a, sa, fmt, "A")
+    n, kb = _mx4_operand(b, sb, fmt, "B")
+    if k != kb:
+        raise ValueError("A and B disagree on K")
+    if d is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        pitch = -(-n // 8) * 8
+        d = torch.empty((m, pitch), dtype=out_dtype, device=dev)
+        if pitch != n:
+            d = d[:, :n]
+    elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (m, n) or d.stride(1) != 1:
+        raise ValueError("d must be a bfloat16 or float32 [M,N] tensor with unit column stride")
+    pitch = max(d.stride(0), -(-n // 8) * 8) if m == 1 else d.stride(0)
+    _run(dev, lib.fp8blk_gemm_mx4, int(fmt) | (OUT_F32 if d.dtype == torch.float32 else 0), m, n, k, _ptr(a), _ptr(sa),
+         _ptr(tensor_sa), _ptr(b), _ptr(sb), _ptr(tensor_sb), _ptr(d), pitch, _stream_handle(stream, dev))
+    return d
+
+
+def mx4_linear_forward(x, qw, sw, fmt, x_scale=None, w_scale=None, stream=None):
+    """Y = X . W^T in 4 bits: X quantised here, W [out,in] ahead (fp8blk_quantize_mx4, ROWWISE)."""
+    qx, sx, _, _ = fp8blk_quantize_mx4(x, fmt, ROWWISE, x_scale, stream=stream)
+    return fp8blk_gemm_mx4(qx, sx, qw, sw, fmt, x_scale, w_scale, stream=stream)
+
+
+def mx4_linear_wgrad(x, dy, fmt, x_scale=None, dy_scale=None, stream=None, out_dtype=torch.bfloat16):
+    """dW = dY^T . X in 4 bits, both quantised here along the tokens."""
+    _, _, qd, sd = fp8blk_quantize_mx4(dy, fmt, COLWISE_T, dy_scale, stream=stream)
+    _, _, qx, sx = fp8blk_quantize_mx4(x, fmt, COLWISE_T, x_scale, stream=stream)
+    return fp8blk_gemm_mx4(qd, sd, qx, sx, fmt, dy_scale, x_scale, stream=stream, out_dtype=out_dtype)
+
+
+def mx4_linear_backward(x, dy, qwT, swT, fmt, x_scale=None, dy_scale=None, w_scale=None, stream=None,
+                        out_dtype=torch.bfloat16):
+    """(dX, dW) of Y = X . W^T in 4 bits: dY quantised once along features and along tokens, X along
+    tokens, W ahead (fp8blk_quantize_mx4, COLWISE_T).  out_dtype: dW's."""
+    qd, sd, qdT, sdT = fp8blk_quantize_mx4(dy, fmt, BOTH, dy_scale, stream=stream)
+    _, _, qxT, sxT = fp8blk_quantize_mx4(x, fmt, COLWISE_T, x_scale, stream=stream)
+    dx = fp8blk_gemm_mx4(qd, sd, qwT, swT, fmt, dy_scale, w_scale, stream=stream)
+    dw = fp8blk_gemm_mx4(qdT, sdT, qxT, sxT, fmt, dy_scale, x_scale, stream=stream, out_dtype=out_dtype)
     return dx, dw

@@ -15,6 +15,8 @@ E5M2 = 4                       # OR into an activation mode: E5M2 codes
 A_E5M2, B_E5M2 = 8, 16         # OR into a GEMM layout: that operand holds E5M2 codes
 OUT_F32 = 32                   # OR into a GEMM layout: fp32 output (unrounded sums)
 FWD, DGRAD, WGRAD = 0, 1, 2
+# fp8blk_mx4_format
+MXFP4, NVFP4 = 0, 1
 
 STATUS_NAMES = {
     0: "FP8BLK_OK", 1: "FP8BLK_ERR_INVALID_ARG", 2: "FP8BLK_ERR_SHAPE", 3: "FP8BLK_ERR_ALIGN",
@@ -61,6 +63,10 @@ def _load() -> ctypes.CDLL:
         "fp8blk_grouped_padded_rows": [I64, I64],
         "fp8blk_quantize_act_1x128_grouped": [P, I64, I64, I64, I, P, I64, P, P, P, P, P],
         "fp8blk_gemm_grouped": [I, I64, P, I64, I64, I64, P, P, P, P, P, I64, P],
+        "fp8blk_mx4_scale_bytes": [I, I64, I64],
+        "fp8blk_quantize_mx4": [P, I64, I64, I64, I, I, P, P, P, P, P, P],
+        "fp8blk_dequantize_mx4": [P, P, I64, I64, I, P, P, I64, P],
+        "fp8blk_gemm_mx4": [I, I64, I64, I64, P, P, P, P, P, P, P, I64, P],
         "fp8blk_gemm_splitk": [I, I64, I64, I64, P, P, P, P, P, I64, I, P, I64, P],
         "fp8blk_gemm_splitk_workspace_bytes": [I, I64, I64, I64, I],
         "fp8blk_gemm_splitk_count": [I, I64, I64, I64],
@@ -75,6 +81,7 @@ def _load() -> ctypes.CDLL:
         fn.restype = {"fp8blk_status_string": ctypes.c_char_p,
                       "fp8blk_amax_ema_workspace_bytes": ctypes.c_int64,
                       "fp8blk_grouped_padded_rows": ctypes.c_int64,
+                      "fp8blk_mx4_scale_bytes": ctypes.c_int64,
                       "fp8blk_gemm_splitk_workspace_bytes": ctypes.c_int64}.get(name, ctypes.c_int)
     return so
 

@@ -122,6 +122,19 @@ fp8blk_status act_outputs(int mode, const uint8_t* q_row, const float* s_row, co
   return FP8BLK_OK;
 }
 
+// The 4-bit formats: only NVFP4 has a tensor scale.
+fp8blk_status check_mx4(int format, const float* tensor_scale) {
+  if (format != FP8BLK_MXFP4 && format != FP8BLK_NVFP4) return FP8BLK_ERR_INVALID_ARG;
+  if (tensor_scale && format != FP8BLK_NVFP4) return FP8BLK_ERR_INVALID_ARG;
+  return (reinterpret_cast<uintptr_t>(tensor_scale) & 3u) ? FP8BLK_ERR_ALIGN : FP8BLK_OK;
+}
+
+// 32-bit TMA coordinates and 32-bit counts of 128 x 128 tiles (and of the narrower GEMM tiles).
+bool mx4_dims_ok(int64_t rows, int64_t cols) {
+  constexpr int64_t kMost = (int64_t(1) << 31) - 512;
+  return rows < kMost && cols < kMost && ((rows + 127) / 128) * ((cols + 127) / 128) < (int64_t(1) << 28);
+}
+
 }  // namespace
 
 extern "C" {
@@ -410,6 +423,112 @@ fp8blk_status fp8blk_gemm_splitk(int layout, int64_t M, int64_t N, int64_t K, co
     if (workspace_bytes < fp8blk::splitk_workspace_bytes(g)) return FP8BLK_ERR_INVALID_ARG;
   }
   return launch_status(fp8blk::launch_gemm(g, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t fp8blk_mx4_scale_bytes(int format, int64_t rows, int64_t k) {
+  if ((format != FP8BLK_MXFP4 && format != FP8BLK_NVFP4) || rows < 0 || k < 0) return -1;
+  const int64_t atom = format == FP8BLK_NVFP4 ? 64 : 128;
+  return ((rows + 127) / 128) * ((k + atom - 1) / atom) * fp8blk::kMx4AtomBytes;
+}
+
+fp8blk_status fp8blk_quantize_mx4(const void* x, int64_t rows, int64_t cols, int64_t ldx, int mode, int format,
+                                  const float* tensor_scale, uint8_t* q_row, uint8_t* s_row, uint8_t* q_colT,
+                                  uint8_t* s_colT, void* stream) {
+  if (mode != FP8BLK_ROWWISE && mode != FP8BLK_COLWISE_T && mode != FP8BLK_BOTH) return FP8BLK_ERR_INVALID_ARG;
+  fp8blk_status st = check_mx4(format, tensor_scale);
+  if (st != FP8BLK_OK) return st;
+  if (rows < 0 || cols < 1 || ((mode & FP8BLK_ROWWISE) && cols % 32 != 0)) return FP8BLK_ERR_SHAPE;
+  if (!mx4_dims_ok(rows, cols)) return FP8BLK_ERR_SHAPE;
+  if (ldx < cols) return FP8BLK_ERR_INVALID_ARG;
+  if (rows == 0) return FP8BLK_OK;
+  if (!x) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(x) || ldx % 8 != 0) return FP8BLK_ERR_ALIGN;
+  fp8blk::Mx4QuantArgs a{};
+  if (mode & FP8BLK_ROWWISE) {
+    if (!q_row || !s_row) return FP8BLK_ERR_INVALID_ARG;
+    if (!aligned16(q_row) || !aligned16(s_row)) return FP8BLK_ERR_ALIGN;
+    a.q_row = q_row;
+    a.s_row = s_row;
+  }
+  if (mode & FP8BLK_COLWISE_T) {
+    if (!q_colT || !s_colT) return FP8BLK_ERR_INVALID_ARG;
+    if (!aligned16(q_colT) || !aligned16(s_colT)) return FP8BLK_ERR_ALIGN;
+    a.q_t = q_colT;
+    a.s_t = s_colT;
+  }
+  if ((st = check_device()) != FP8BLK_OK) return st;
+  a.x = static_cast<const uint16_t*>(x);
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.nv = format == FP8BLK_NVFP4;
+  a.tensor_scale = tensor_scale;
+  a.timeout_ns = wait_timeout_ns();
+  a.err = error_word();
+  if (!a.err) return FP8BLK_ERR_CUDA;
+  a.pdl = pdl_enabled();
+  a.max_ctas = env_int("FP8BLK_QUANT_MAX_CTAS", 0);
+  return launch_status(fp8blk::launch_mx4_quant(a, static_cast<cudaStream_t>(stream)));
+}
+
+fp8blk_status fp8blk_dequantize_mx4(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, int format,
+                                    const float* tensor_scale, void* y, int64_t ldy, void* stream) {
+  fp8blk_status st = check_mx4(format, tensor_scale);
+  if (st != FP8BLK_OK) return st;
+  if (rows < 0 || cols < 1 || cols % 32 != 0 || !mx4_dims_ok(rows, cols)) return FP8BLK_ERR_SHAPE;
+  if (ldy < cols) return FP8BLK_ERR_INVALID_ARG;
+  if (rows == 0) return FP8BLK_OK;
+  if (!q || !s || !y) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(s) || !aligned16(y) || ldy % 8 != 0) return FP8BLK_ERR_ALIGN;
+  if ((st = check_device()) != FP8BLK_OK) return st;
+  const fp8blk::Mx4DequantArgs a{q, s, tensor_scale, rows, cols, format == FP8BLK_NVFP4, static_cast<uint16_t*>(y),
+                                 ldy, pdl_enabled()};
+  return launch_status(fp8blk::launch_mx4_dequant(a, static_cast<cudaStream_t>(stream)));
+}
+
+fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const uint8_t* a, const uint8_t* sa,
+                              const float* tensor_sa, const uint8_t* b, const uint8_t* sb, const float* tensor_sb,
+                              void* d, int64_t ldd, void* stream) {
+  const bool out_f32 = (format & FP8BLK_OUT_F32) != 0;
+  format &= ~FP8BLK_OUT_F32;
+  fp8blk_status st = check_mx4(format, tensor_sa);
+  if (st == FP8BLK_OK) st = check_mx4(format, tensor_sb);
+  if (st != FP8BLK_OK) return st;
+  if (M < 0 || N < 1 || K < 0 || K % 32 != 0) return FP8BLK_ERR_SHAPE;
+  if (!mx4_dims_ok(M, N) || !mx4_dims_ok(M, K) || !mx4_dims_ok(N, K)) return FP8BLK_ERR_SHAPE;
+  if (ldd < N) return FP8BLK_ERR_INVALID_ARG;
+  if (M == 0) return FP8BLK_OK;
+  if (!d || (K > 0 && (!a || !sa || !b || !sb))) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(d) ||
+      ldd % (out_f32 ? 4 : 8) != 0)
+    return FP8BLK_ERR_ALIGN;
+  if ((st = check_device()) != FP8BLK_OK) return st;
+  if (K == 0) {   // an empty sum (the weight gradient of no tokens)
+    const size_t size = out_f32 ? 4 : 2;
+    return launch_status(cudaMemset2DAsync(d, ldd * size, 0, N * size, M, static_cast<cudaStream_t>(stream)));
+  }
+  fp8blk::Mx4GemmArgs g{};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.nv = format == FP8BLK_NVFP4;
+  g.a = a;
+  g.sa = sa;
+  g.b = b;
+  g.sb = sb;
+  g.tsa = tensor_sa;
+  g.tsb = tensor_sb;
+  g.d = d;
+  g.ldd = ldd;
+  g.out_f32 = out_f32;
+  g.timeout_ns = wait_timeout_ns();
+  g.err = error_word();
+  if (!g.err) return FP8BLK_ERR_CUDA;
+  g.inject_stall = env_int("FP8BLK_TEST_INJECT_STALL", 0) != 0;
+  g.group_m = env_int("FP8BLK_GEMM_GROUP_M", 0);
+  g.pdl = pdl_enabled();
+  g.max_ctas = env_int("FP8BLK_GEMM_MAX_CTAS", 0);
+  return launch_status(fp8blk::launch_gemm_mx4(g, static_cast<cudaStream_t>(stream)));
 }
 
 int64_t fp8blk_amax_ema_workspace_bytes(int64_t rows) {

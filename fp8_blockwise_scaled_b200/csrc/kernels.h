@@ -134,6 +134,57 @@ struct GroupedGemmArgs {
 
 cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, cudaStream_t stream);
 
+// 4-bit microscaled quantisation (mx4_quant.cu) and products (mx4_gemm.cu).
+constexpr int kMx4AtomBytes = 512;   // scales of 128 rows x 4 blocks
+struct Mx4QuantArgs {
+  const uint16_t* x;          // [rows][ldx] bf16
+  int64_t rows, cols, ldx;
+  int nv;                     // 1 = NVFP4, 0 = MXFP4
+  const float* tensor_scale;  // NVFP4: device scalar, null = 1
+  uint8_t* q_row;             // [rows][cols/2], null = not written
+  uint8_t* s_row;             // [rows/128][cols/(4 block)][512]
+  uint8_t* q_t;               // [cols][padded rows/2], padded to whole 32, null = not written
+  uint8_t* s_t;               // [cols/128][padded rows/(4 block)][512]
+  uint64_t timeout_ns;
+  unsigned int* err;
+  int pdl;
+  int max_ctas;
+};
+cudaError_t launch_mx4_quant(const Mx4QuantArgs& a, cudaStream_t stream);
+
+struct Mx4DequantArgs {
+  const uint8_t* q;           // [rows][cols/2]
+  const uint8_t* s;
+  const float* tensor_scale;
+  int64_t rows, cols;
+  int nv;
+  uint16_t* y;                // [rows][ldy] bf16
+  int64_t ldy;
+  int pdl;
+};
+cudaError_t launch_mx4_dequant(const Mx4DequantArgs& a, cudaStream_t stream);
+
+struct Mx4GemmArgs {
+  int64_t M, N, K;
+  int nv;                     // 1 = NVFP4, 0 = MXFP4
+  const uint8_t* a;           // [M][K/2]
+  const uint8_t* sa;          // [M/128][K/(4 block)][512]
+  const uint8_t* b;           // [N][K/2]
+  const uint8_t* sb;          // [N/128][K/(4 block)][512]
+  const float* tsa;           // NVFP4: tensor scales (device scalars), null = 1
+  const float* tsb;
+  void* d;                    // [M][ldd] bf16, or fp32 when out_f32
+  int64_t ldd;
+  int out_f32;
+  uint64_t timeout_ns;
+  int inject_stall;
+  int group_m;
+  int pdl;
+  int max_ctas;
+  unsigned int* err;
+};
+cudaError_t launch_gemm_mx4(const Mx4GemmArgs& g, cudaStream_t stream);
+
 // y[i] = bf16_round_nearest_even(x[i]) for i < n (x, y 16-byte aligned).
 cudaError_t launch_round_bf16(const float* x, int64_t n, uint16_t* y, int pdl, cudaStream_t stream);
 

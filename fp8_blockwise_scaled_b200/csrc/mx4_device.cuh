@@ -1,0 +1,139 @@
+// 4-bit microscaled formats: code conversions and the tcgen05 forms that take
+// block scales.
+//
+// Codes are E2M1 (+-0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, the element of
+// the lower index in the low nibble.  A row's scales are one byte a block:
+//   MXFP4  32 values, E8M0 (2^(byte - 127));
+//   NVFP4  16 values, E4M3, below one fp32 scale for the tensor.
+// Scales are stored in the order in which tensor memory takes them, as atoms of
+// 512 bytes for 128 rows x 4 blocks: row r, block j at byte
+// (r % 32) * 16 + (r / 32) * 4 + j, so that one tcgen05.cp (32 lanes x 16 bytes)
+// puts an atom into four columns.
+#pragma once
+
+#include <stdint.h>
+
+#include "device.cuh"
+#include "kernels.h"
+
+namespace fp8blk {
+
+// Values of a block, and elements of a row that one atom covers.
+template <bool kNv>
+__host__ __device__ constexpr int mx4_block() { return kNv ? 16 : 32; }
+template <bool kNv>
+__host__ __device__ constexpr int mx4_atom_elems() { return 4 * mx4_block<kNv>(); }
+
+// Eight values -> eight codes, x[0] in the lowest nibble (round to nearest
+// even, values above 6 saturate).
+__device__ __forceinline__ uint32_t cvt8_e2m1(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// One value -> its E4M3 code (saturating), and an E4M3 code's value.
+__device__ __forceinline__ uint32_t cvt_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(x));
+  return r & 0xFFu;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code)));
+  float f;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
+  return f;
+}
+
+// An E8M0 byte's value, 2^(byte - 127) (byte 0: the subnormal 2^-127).
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+}
+
+// Copies one scale atom (32 lanes x 16 bytes) from shared memory into four
+// columns of tensor memory, the same in all four lane quarters.
+__device__ __forceinline__ void tmem_cp_atom(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void tmem_cp_atom_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Shared-memory descriptor of a scale atom: no swizzle, 8-row groups (16 bytes
+// a row) 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_atom(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;             // leading byte offset (one 16-byte column: unused)
+  d |= static_cast<uint64_t>(128 >> 4) << 32;      // stride byte offset
+  d |= static_cast<uint64_t>(1) << 46;             // descriptor version for sm_100
+  return d;
+}
+
+// Instruction descriptor of the block-scaled 4-bit products: E2M1 A and B,
+// fp32 D, both K-major, tile m x n; scales E4M3 (NVFP4) or E8M0 (MXFP4).
+__host__ __device__ constexpr uint32_t idesc_mx4(int m, int n, bool nv) {
+  return (1u << 7) | (1u << 10)                      // A, B format: E2M1
+         | (static_cast<uint32_t>(n >> 3) << 17)     // N / 8
+         | (nv ? 0u : 1u << 23)                      // scale format: E8M0 where set
+         | (static_cast<uint32_t>(m >> 7) << 27);    // M / 128
+}
+
+// The bits of that descriptor that name the byte pair of a scale word which an
+// instruction of 64 values with two scales (MXFP4) takes: 0 or 2.
+__host__ __device__ constexpr uint32_t idesc_scale_id(uint32_t id) { return (id << 4) | (id << 29); }
+
+// D[tmem] (+)= (A scaled by sfa) . (B scaled by sfb)^T over 64 values of K.
+template <bool kNv>
+__device__ __forceinline__ void umma_mx4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (kNv)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// The same across a pair of CTAs (M = 256).
+template <bool kNv>
+__device__ __forceinline__ void umma_mx4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (kNv)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+}  // namespace fp8blk

@@ -1,0 +1,448 @@
+// Products of 4-bit microscaled operands for sm_100a (tcgen05 block-scaled MMA).
+//
+//   D[m][n] = ga gb sum_k a[m][k] sfa(m, block of k) b[n][k] sfb(n, block of k)
+//
+// The tensor cores apply the block scales themselves, so a tile's whole K loop
+// accumulates in TMEM in fp32 and the epilogue multiplies once by the tensors'
+// scales and rounds once.  What is left to feed is the operands (128 bytes of
+// codes a row and stage: 256 values of K) and their scales: a stage's scale
+// atoms arrive by TMA next to the codes and are copied from shared memory to
+// TMEM by tcgen05.cp, in the order of the MMAs that read them.  Two sets of
+// scale columns alternate; a set is rewritten once the MMAs that read it have
+// completed (their commit).
+//
+// Warp roles (256 threads): warp 0 loads, warp 1 owns TMEM and issues copies
+// and MMAs, warps 4-7 drain the accumulators (two of them alternate, so a
+// tile's epilogue runs under the next tile's K loop).
+//
+// gemm_mx4_kernel: one CTA per SM, 128 x BN tiles.  kSwap exchanges the
+// operands' roles for few rows of a (decoding): 128 rows of b are the MMA's
+// M side and BN = 16 .. 128 rows of a its N side, so the tile is as high as the
+// weights are and hardly wider than the tokens.
+//
+// Every wait is bounded as in gemm.cu.
+#include <cudaTypedefs.h>
+
+#include "gemm_device.cuh"
+#include "gemm_host.h"
+#include "kernels.h"
+#include "mx4_device.cuh"
+
+namespace fp8blk {
+
+namespace {
+
+constexpr int kMxThreads = 256;
+constexpr int kStageK = 256;             // values of K in a stage: 128 bytes of codes
+constexpr int kEpiWarp0 = 4;
+
+struct Mx4Params {
+  int64_t M, N, K;          // rows of a, rows of b, contraction
+  const float* tsa;         // NVFP4: tensor scales (null = 1)
+  const float* tsb;
+  void* d;
+  int64_t ldd;
+  int out_f32;
+  int group_m;
+  uint64_t timeout_ns;
+  unsigned int* err;
+  int inject_stall;
+};
+
+template <int BN, bool kNv>
+struct MxCfg {
+  static constexpr int kAtoms = kNv ? 4 : 2;              // scale atoms of 128 rows in a stage
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kBBytes = BN * 128;
+  static constexpr int kSfBytes = kAtoms * kMx4AtomBytes;    // of each operand
+  static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
+  static constexpr int kStages = BN == 128 ? 5 : (BN == 64 ? 6 : 8);
+  static constexpr int kOutBytes = 4 * 2 * 4096;          // two 32-row boxes of 128 bytes for each epilogue warp
+  static constexpr int kSetCols = 2 * kAtoms * 4;         // TMEM columns of one set of scales
+  static constexpr int kTmemUsed = 2 * BN + 2 * kSetCols;
+  static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : (kTmemUsed <= 256 ? 256 : 512);
+  static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+};
+
+struct MxCtrl {
+  uint64_t full[8], empty[8];
+  uint64_t tfull[2], tempty[2];
+  uint64_t sfree[2];                     // the MMAs that read this set of scale columns are done
+  uint64_t mma_done;
+  uint64_t never;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int BN, bool kNv>
+constexpr int mx_smem_bytes() {
+  using C = MxCfg<BN, kNv>;
+  return 1024 + C::kStages * C::kStageBytes + C::kOutBytes + static_cast<int>(sizeof(MxCtrl));
+}
+
+__device__ __forceinline__ void bulk_wait_group_read1() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+
+// One warp's 32 rows of a finished accumulator (kCols columns from `taddr`) to
+// d: times alpha, rounded to bf16 (boxes of 64 columns) or as fp32 (boxes of
+// 32), through the warp's two staging boxes and TMA stores, which clip at d's
+// last row and column.  A TMA store clips columns in units of 16 bytes: where N
+// is no multiple of them, the last columns are stored one by one, so that
+// nothing behind column N is written.  `stores`: boxes this warp has staged.
+template <int kCols>
+__device__ __forceinline__ void store_tile(const Mx4Params& p, const CUtensorMap* tm_d, uint8_t* stg, uint32_t taddr,
+                                           float alpha, int64_t row, int64_t col, int lane, uint32_t& stores) {
+  const bool inside = row < p.M;         // a box starts inside d or is not stored
+#pragma unroll 1
+  for (int c = 0; c < kCols; c += 64) {
+    uint32_t r[2][32];
+    tmem_ld_32x32b_x32(taddr + c, r[0]);
+    tmem_ld_32x32b_x32(taddr + c + 32, r[1]);
+    tmem_wait_ld32(r[0]);
+    tmem_wait_ld32(r[1]);
+    if (col + c + 64 > p.N && p.N % (p.out_f32 ? 4 : 8) != 0) {
+      if (row + lane < p.M) {
+        const int64_t at = (row + lane) * p.ldd + col + c;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+          if (col + c + j < p.N) {
+            const float v = __uint_as_float(r[j >> 5][j & 31]) * alpha;
+            if (p.out_f32)
+              static_cast<float*>(p.d)[at + j] = v;
+            else
+              static_cast<__nv_bfloat16*>(p.d)[at + j] = __float2bfloat16_rn(v);
+          }
+        }
+      }
+      __syncwarp();
+    } else if (p.out_f32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint8_t* box = stg + (stores & 1) * 4096;
+        if (lane == 0) bulk_wait_group_read1();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_float4(__uint_as_float(r[h][4 * j]) * alpha, __uint_as_float(r[h][4 * j + 1]) * alpha,
+                          __uint_as_float(r[h][4 * j + 2]) * alpha, __uint_as_float(r[h][4 * j + 3]) * alpha);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (inside && col + c + 32 * h < p.N)
+            tma_store_2d(tm_d, box, static_cast<int>(col) + c + 32 * h, static_cast<int>(row));
+          bulk_commit_group();
+        }
+        ++stores;
+      }
+    } else {
+      uint8_t* box = stg + (stores & 1) * 4096;
+      if (lane == 0) bulk_wait_group_read1();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t* q = r[j >> 2] + 8 * (j & 3);
+        *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(
+            pack_bf16x2(__uint_as_float(q[0]) * alpha, __uint_as_float(q[1]) * alpha),
+            pack_bf16x2(__uint_as_float(q[2]) * alpha, __uint_as_float(q[3]) * alpha),
+            pack_bf16x2(__uint_as_float(q[4]) * alpha, __uint_as_float(q[5]) * alpha),
+            pack_bf16x2(__uint_as_float(q[6]) * alpha, __uint_as_float(q[7]) * alpha));
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (inside && col + c < p.N) tma_store_2d(tm_d, box, static_cast<int>(col) + c, static_cast<int>(row));
+        bulk_commit_group();
+      }
+      ++stores;
+    }
+  }
+}
+
+}  // namespace
+
+template <int BN, bool kNv, bool kSwap>
+__global__ void __launch_bounds__(kMxThreads, 1)
+    gemm_mx4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                    const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
+                    const __grid_constant__ CUtensorMap tm_d, const Mx4Params p) {
+  using C = MxCfg<BN, kNv>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem_out = smem + C::kStages * C::kStageBytes;
+  MxCtrl* ctrl = reinterpret_cast<MxCtrl*>(smem_out + C::kOutBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The MMA's M side in tiles of 128 rows, its N side in tiles of BN.
+  const int num_mb = static_cast<int>(((kSwap ? p.N : p.M) + 127) / 128);
+  const int num_nb = static_cast<int>(((kSwap ? p.M : p.N) + BN - 1) / BN);
+  const int kblocks = static_cast<int>((p.K + kStageK - 1) / kStageK);
+  const int tiles = num_mb * num_nb;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], 4);
+      mbar_init(&ctrl->sfree[b], 1);
+    }
+    mbar_init(&ctrl->mma_done, 1);
+    mbar_init(&ctrl->never, 1);
+    ctrl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctrl->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const uint32_t tmem_base = ctrl->tmem_base;
+  volatile int* abort = &ctrl->abort;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const CUtensorMap* ma = kSwap ? &tm_b : &tm_a;
+      const CUtensorMap* mb_ = kSwap ? &tm_a : &tm_b;
+      const CUtensorMap* msa = kSwap ? &tm_sb : &tm_sa;
+      const CUtensorMap* msb = kSwap ? &tm_sa : &tm_sb;
+      tma_prefetch_map(ma);
+      tma_prefetch_map(mb_);
+      tma_prefetch_map(msa);
+      tma_prefetch_map(msb);
+      Ring<C::kStages> st;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < tiles; u += gridDim.x) {
+        int mb, nb;
+        tile_coords(u, num_mb, num_nb, p.group_m, mb, nb);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait_bounded(&ctrl->empty[st.idx], st.phase ^ 1u, abort, p.timeout_ns, p.err)) {
+            ok = false;
+            break;
+          }
+          uint8_t* stage = smem + st.idx * C::kStageBytes;
+          uint64_t* full = &ctrl->full[st.idx];
+          mbar_arrive_expect_tx(full, C::kStageBytes);
+          tma_load_2d(stage, ma, full, kb * 128, mb * 128);
+          tma_load_2d(stage + C::kABytes, mb_, full, kb * 128, nb * BN);
+          // Scale maps: rows of 128-row blocks, columns of 8-byte words, 64 to an atom.
+          tma_load_2d(stage + C::kABytes + C::kBBytes, msa, full, kb * C::kAtoms * 64, mb);
+          tma_load_2d(stage + C::kABytes + C::kBBytes + C::kSfBytes, msb, full, kb * C::kAtoms * 64, nb * BN / 128);
+          ++issued;
+          st.next();
+        }
+      }
+      const int64_t first = issued > C::kStages ? issued - C::kStages : 0;
+      for (int64_t j = first; j < issued; ++j)
+        mbar_wait_bounded(&ctrl->full[j % C::kStages], static_cast<uint32_t>((j / C::kStages) & 1), nullptr,
+                          p.timeout_ns, p.err);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = idesc_mx4(128, BN, kNv);
+    const uint32_t smem0 = smem_addr(smem);
+    Ring<C::kStages> st;
+    Ring<2> acc, set;
+    bool ok = true;
+    if (p.inject_stall) ok = mbar_wait_bounded(&ctrl->never, 0, abort, p.timeout_ns, p.err);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    for (int u = blockIdx.x; ok && u < tiles; u += gridDim.x) {
+      if (!__all_sync(0xFFFFFFFFu,
+                      mbar_wait_bounded<false>(&ctrl->tempty[acc.idx], acc.phase ^ 1u, abort, p.timeout_ns, p.err)))
+        break;
+      const uint32_t d_tmem = tmem_base + acc.idx * BN;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        const bool got = mbar_wait_bounded<false>(&ctrl->full[st.idx], st.phase, abort, p.timeout_ns, p.err) &&
+                         mbar_wait_bounded<false>(&ctrl->sfree[set.idx], set.phase ^ 1u, abort, p.timeout_ns, p.err);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t a_addr = smem0 + st.idx * C::kStageBytes;
+        const uint32_t sf_addr = a_addr + C::kABytes + C::kBBytes;
+        const uint64_t adesc = smem_desc_kmajor_sw128(a_addr);
+        const uint64_t bdesc = smem_desc_kmajor_sw128(a_addr + C::kABytes);
+        const uint64_t sfdesc = smem_desc_atom(sf_addr);
+        const uint32_t sfa = tmem_base + 2 * BN + set.idx * C::kSetCols, sfb = sfa + C::kAtoms * 4;
+        const int steps = static_cast<int>(min((p.K - static_cast<int64_t>(kb) * kStageK + 63) / 64, int64_t{4}));
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < C::kAtoms; ++i) {
+            tmem_cp_atom(sfa + 4 * i, sfdesc + i * (kMx4AtomBytes >> 4));
+            tmem_cp_atom(sfb + 4 * i, sfdesc + ((C::kSfBytes + i * kMx4AtomBytes) >> 4));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k < steps) {
+              const int atom = kNv ? k : k >> 1;
+              umma_mx4<kNv>(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc | idesc_scale_id(kNv ? 0 : 2 * (k & 1)),
+                            sfa + 4 * atom, sfb + 4 * atom, (kb | k) != 0);
+            }
+          }
+          umma_commit(&ctrl->empty[st.idx]);
+          umma_commit(&ctrl->sfree[set.idx]);
+          if (kb == kblocks - 1) umma_commit(&ctrl->tfull[acc.idx]);
+        }
+        __syncwarp();
+        st.next();
+        set.next();
+      }
+      acc.next();
+    }
+    if (leader) umma_commit(&ctrl->mma_done);
+    __syncwarp();
+    mbar_wait_bounded(&ctrl->mma_done, 0, nullptr, p.timeout_ns, p.err);
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint8_t* stg = smem_out + quarter * 8192;
+    const float alpha = (p.tsa ? __ldg(p.tsa) : 1.0f) * (p.tsb ? __ldg(p.tsb) : 1.0f);
+    Ring<2> acc;
+    uint32_t stores = 0;
+    for (int u = blockIdx.x; u < tiles; u += gridDim.x) {
+      int mb, nb;
+      tile_coords(u, num_mb, num_nb, p.group_m, mb, nb);
+      if (!__all_sync(0xFFFFFFFFu,
+                      mbar_wait_bounded<false>(&ctrl->tfull[acc.idx], acc.phase, abort, p.timeout_ns, p.err)))
+        break;
+      tc_fence_after_sync();
+      const uint32_t taddr = lanes + acc.idx * BN;
+      if constexpr (!kSwap) {
+        store_tile<BN>(p, &tm_d, stg, taddr, alpha, static_cast<int64_t>(mb) * 128 + quarter * 32,
+                       static_cast<int64_t>(nb) * BN, lane, stores);
+      } else {
+        // The tile is D transposed: this lane is column n, TMEM columns are rows of D.
+        const int64_t n = static_cast<int64_t>(mb) * 128 + quarter * 32 + lane;
+        const int64_t m0 = static_cast<int64_t>(nb) * BN;
+        const int rows = static_cast<int>(min(p.M - m0, static_cast<int64_t>(BN)));
+        for (int c = 0; c < rows; c += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(taddr + c, r);
+          tmem_wait_ld16(r);
+          if (n < p.N) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (c + j < rows) {
+                const float v = __uint_as_float(r[j]) * alpha;
+                const int64_t at = (m0 + c + j) * p.ldd + n;
+                if (p.out_f32)
+                  static_cast<float*>(p.d)[at] = v;
+                else
+                  static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16_rn(v);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->tempty[acc.idx]);
+      acc.next();
+    }
+    if (!kSwap && lane == 0) bulk_wait_group0();
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+namespace {
+
+bool encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t inner, int64_t outer,
+                int64_t pitch_bytes, int box_inner, int box_outer, CUtensorMapSwizzle swizzle,
+                CUtensorMapL2promotion promotion) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Codes [rows][k/2 bytes], boxes of 128 bytes x box_rows in the 128-byte swizzle.
+bool codes_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t k, int box_rows) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, k / 2, rows, k / 2, 128, box_rows,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// Scale atoms [rows/128][atoms][512 bytes] as 8-byte words; a box is one stage's atoms of row_blocks blocks.
+bool scales_map(CUtensorMap* map, const uint8_t* s, int64_t rows, int64_t k, bool nv, int row_blocks) {
+  const int64_t atoms = nv ? (k + 63) / 64 : (k + 127) / 128;
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, s, atoms * 64, (rows + 127) / 128, atoms * kMx4AtomBytes,
+                    (nv ? 4 : 2) * 64, row_blocks, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// The output, boxes of 32 rows x 128 bytes in the 128-byte swizzle.
+bool mx_out_map(CUtensorMap* map, const Mx4GemmArgs& g) {
+  const int size = g.out_f32 ? 4 : 2;
+  return encode_map(map, g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.d, g.N, g.M,
+                    g.ldd * size, 128 / size, 32, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+Mx4Params mx_params(const Mx4GemmArgs& g, int64_t num_mb) {
+  Mx4Params p{g.M, g.N, g.K, g.tsa, g.tsb, g.d, g.ldd, g.out_f32, 0, g.timeout_ns, g.err, g.inject_stall};
+  p.group_m = static_cast<int>(num_mb < 8 ? num_mb : (g.group_m > 0 ? g.group_m : 8));
+  return p;
+}
+
+template <int BN, bool kNv, bool kSwap>
+cudaError_t launch_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
+  static PerContext<int> smem_set;
+  constexpr int kSmem = mx_smem_bytes<BN, kNv>();
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_kernel<BN, kNv, kSwap>, kSmem); e != cudaSuccess) return e;
+  CUtensorMap ta, tb, tsa, tsb, td;
+  if (!codes_map(&ta, g.a, g.M, g.K, kSwap ? BN : 128) || !codes_map(&tb, g.b, g.N, g.K, kSwap ? 128 : BN) ||
+      !scales_map(&tsa, g.sa, g.M, g.K, kNv, 1) || !scales_map(&tsb, g.sb, g.N, g.K, kNv, 1) || !mx_out_map(&td, g))
+    return cudaErrorInvalidValue;
+  const int64_t num_mb = ((kSwap ? g.N : g.M) + 127) / 128, num_nb = ((kSwap ? g.M : g.N) + BN - 1) / BN;
+  const Mx4Params p = mx_params(g, num_mb);
+  int64_t ctas = num_sms();
+  if (g.max_ctas > 0 && g.max_ctas < ctas) ctas = g.max_ctas;
+  if (num_mb * num_nb < ctas) ctas = num_mb * num_nb;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(kMxThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  cfg.numAttrs = set_pdl_attr(attr, g.pdl);
+  cfg.attrs = attr;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<BN, kNv, kSwap>, ta, tb, tsa, tsb, td, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool kNv>
+cudaError_t launch_mx4_fmt(const Mx4GemmArgs& g, cudaStream_t stream) {
+  if (g.M <= 16) return launch_mx4<16, kNv, true>(g, stream);
+  if (g.M <= 32) return launch_mx4<32, kNv, true>(g, stream);
+  if (g.M <= 64) return launch_mx4<64, kNv, true>(g, stream);
+  return launch_mx4<128, kNv, false>(g, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
+  return g.nv ? launch_mx4_fmt<true>(g, stream) : launch_mx4_fmt<false>(g, stream);
+}
+
+}  // namespace fp8blk

@@ -22,7 +22,8 @@
  *    bf16 inputs are raw bfloat16 bit patterns (uint16).  E4M3 codes are
  *    float8_e4m3fn bytes.  Scales are IEEE binary32.
  *  - Every dimension must be a positive multiple of 128 (FP8BLK_ERR_SHAPE),
- *    except where an entry point says otherwise (rows sorted by group).
+ *    except where an entry point says otherwise (rows sorted by group, the
+ *    4-bit formats).
  *    Pointers must be 16-byte aligned and leading dimensions must give
  *    16-byte aligned rows (FP8BLK_ERR_ALIGN).
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
@@ -322,6 +323,79 @@ int64_t fp8blk_gemm_splitk_workspace_bytes(int layout, int64_t M, int64_t N, int
  * each, else 1.  0 for an invalid layout or shape or an unsupported device.
  */
 int fp8blk_gemm_splitk_count(int layout, int64_t M, int64_t N, int64_t K);
+
+/*
+ * 4-bit microscaled formats.  Codes are E2M1 (+-0, 0.5, 1, 1.5, 2, 3, 4, 6), two
+ * to a byte, the lower index in the low nibble; blocks of consecutive values
+ * along the contraction share a one-byte scale:
+ *   FP8BLK_MXFP4  32 values, E8M0 (2^(byte - 127)); the OCP Microscaling rule
+ *                   scale = 2^clamp(floor(log2 amax) - 2, -127, 127),
+ *                   q = E2M1_round_nearest_even(clamp(x / scale, -6, 6))
+ *   FP8BLK_NVFP4  16 values, E4M3, below one fp32 scale g for the tensor
+ *                 (device scalar, > 0, null = 1; amax of the tensor / 2688
+ *                 uses the whole range):
+ *                   sf = E4M3_round_nearest_even(min(fl32(fl32(amax / 6) / g), 448)),
+ *                   d = fl32(sf * g),
+ *                   q = E2M1_round_nearest_even(clamp(fl32(x / d), -6, 6)), zeros where sf is 0
+ *                 (|x| / g below 2^100 and g at least 1e-12, else unspecified codes).
+ *
+ * Scales are laid out as the tensor cores take them, for a [R][K] operand as
+ *   [ceil(R / 128)][ceil(K / (4 * block))][512 bytes],
+ * row r and block j of an atom (128 rows x 4 blocks) at byte
+ * (r % 32) * 16 + (r % 128 / 32) * 4 + j; places of rows and blocks that do not
+ * exist hold zeros (fp8blk_quantize_mx4 writes them).  fp8blk_mx4_scale_bytes
+ * gives the size; -1 for a bad format or a negative size.
+ */
+typedef enum {
+  FP8BLK_MXFP4 = 0,
+  FP8BLK_NVFP4 = 1
+} fp8blk_mx4_format;
+
+int64_t fp8blk_mx4_scale_bytes(int format, int64_t rows, int64_t k);
+
+/*
+ * 4-bit quantisation of activations, weights or gradients.
+ *   x        [rows][ldx] bf16, rows >= 0 and cols >= 1 (any numbers), ldx a multiple of 8.
+ *   mode     FP8BLK_ROWWISE, FP8BLK_COLWISE_T or FP8BLK_BOTH (from one read of x).
+ *   ROWWISE  (cols a multiple of 32) blocks along the columns:
+ *            q_row [rows][cols/2], s_row as above for [rows][cols].
+ *   COLWISE_T blocks along the rows, codes transposed, the rows padded with
+ *            zeros to P = rows rounded up to a multiple of 32:
+ *            q_colT [cols][P/2], s_colT as above for [cols][P].
+ * Errors: FP8BLK_ERR_INVALID_ARG for a bad mode or format, a tensor scale with
+ * FP8BLK_MXFP4, ldx < cols or a missing output; FP8BLK_ERR_SHAPE;
+ * FP8BLK_ERR_ALIGN (codes, scales and x 16-byte aligned).
+ */
+fp8blk_status fp8blk_quantize_mx4(const void* x, int64_t rows, int64_t cols, int64_t ldx, int mode, int format,
+                                  const float* tensor_scale, uint8_t* q_row, uint8_t* s_row, uint8_t* q_colT,
+                                  uint8_t* s_colT, void* stream);
+
+/*
+ * The values of 4-bit codes: y[r][c] = bf16(fl32(q * d)), d = the block's scale
+ * (fl32(sf * g) for FP8BLK_NVFP4).  q [rows][cols/2] and s as above (also a
+ * COLWISE_T pair, with its rows = cols and cols = P); cols a multiple of 32;
+ * y [rows][ldy] bf16, 16-byte aligned, ldy a multiple of 8.
+ */
+fp8blk_status fp8blk_dequantize_mx4(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, int format,
+                                    const float* tensor_scale, void* y, int64_t ldy, void* stream);
+
+/*
+ * Product of 4-bit operands on the block-scaled tensor cores:
+ *   D[m][n] = bf16( ga * gb * sum_k a[m][k] sfa[m][k / block] b[n][k] sfb[n][k / block] ),
+ * accumulated in fp32 over the whole of K.
+ *   format   FP8BLK_MXFP4 or FP8BLK_NVFP4, optionally OR-ed with
+ *            FP8BLK_OUT_F32 (fp32 output, unrounded).
+ *   a, sa    [M][K/2] codes and their scales;  b, sb  [N][K/2].
+ *   tensor_sa, tensor_sb   the tensors' scales (FP8BLK_NVFP4; device scalars, null = 1).
+ *   M >= 0 and N >= 1 (any numbers), K a multiple of 32 (0: zeros are written).
+ *   d        [M][ldd], ldd >= N a multiple of 8 (of 4 for fp32), 16-byte aligned.
+ * The passes of a linear layer are those of fp8blk_gemm: FWD a = X rowwise,
+ * b = W rowwise; DGRAD a = dY rowwise, b = W colwise_T; WGRAD a = dY colwise_T,
+ * b = X colwise_T.
+ */
+fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const uint8_t* a, const uint8_t* sa,
+                              const float* tensor_sa, const uint8_t* b, const uint8_t* sb, const float* tensor_sb,
+                              void* d, int64_t ldd, void* stream);
 
 /*
  * Per-tensor delayed scaling ([EXPL] "核心挑战：Scale Factor 管理", FP8Linear):
