@@ -65,11 +65,12 @@ E4M3 = torch.float8_e4m3fn
 E5M2_DTYPE = torch.float8_e5m2
 
 
-def _stream_handle(stream, device=None) -> ctypes.c_void_p:
+def _stream_handle(stream, device=None) -> int:
     """The cudaStream_t to launch on: `stream`, else the current stream of `device`."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
+        # The current stream's handle, without a Stream object: every call of the library asks for it.
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _need_cuda(*tensors) -> torch.device:
@@ -90,8 +91,11 @@ def _need_cuda(*tensors) -> torch.device:
 def _run(device, fn, *args) -> None:
     """Calls a C entry point with `device` current, so that the library's device
     check, its per-device state and the launch all refer to the tensors' GPU."""
-    with torch.cuda.device(device):
+    if device.index == torch.cuda.current_device():
         check(fn(*args))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args))
 
 
 def _out(t, shape, dtype, device):
@@ -102,8 +106,8 @@ def _out(t, shape, dtype, device):
     return t
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _bf16_2d(x):

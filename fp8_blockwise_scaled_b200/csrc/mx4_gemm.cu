@@ -33,6 +33,7 @@ namespace fp8blk {
 namespace {
 
 constexpr int kMxThreads = 256;
+constexpr int kMxPairThreads = 384;      // eight epilogue warps
 constexpr int kStageK = 256;             // values of K in a stage: 128 bytes of codes
 constexpr int kEpiWarp0 = 4;
 
@@ -84,79 +85,80 @@ __device__ __forceinline__ void bulk_wait_group_read1() {
   asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 
-// One warp's 32 rows of a finished accumulator (kCols columns from `taddr`) to
-// d: times alpha, rounded to bf16 (boxes of 64 columns) or as fp32 (boxes of
-// 32), through the warp's two staging boxes and TMA stores, which clip at d's
-// last row and column.  A TMA store clips columns in units of 16 bytes: where N
-// is no multiple of them, the last columns are stored one by one, so that
-// nothing behind column N is written.  `stores`: boxes this warp has staged.
-template <int kCols>
-__device__ __forceinline__ void store_tile(const Mx4Params& p, const CUtensorMap* tm_d, uint8_t* stg, uint32_t taddr,
-                                           float alpha, int64_t row, int64_t col, int lane, uint32_t& stores) {
+// 64 columns of one warp's 32 accumulator rows.
+__device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[2][32]) {
+  tmem_ld_32x32b_x32(taddr, r[0]);
+  tmem_ld_32x32b_x32(taddr + 32, r[1]);
+  tmem_wait_ld32(r[0]);
+  tmem_wait_ld32(r[1]);
+}
+
+// Those columns to d (row, col: the chunk's first): times alpha, rounded to bf16
+// (one box of 64 columns) or as fp32 (two boxes of 32), through the warp's two
+// staging boxes and TMA stores, which clip at d's last row and column.  A TMA
+// store clips columns in units of 16 bytes: where N is no multiple of them, the
+// last columns are stored one by one, so that nothing behind column N is
+// written.  `stores`: boxes this warp has staged.
+__device__ __forceinline__ void store_chunk(const Mx4Params& p, const CUtensorMap* tm_d, uint8_t* stg,
+                                            const uint32_t (&r)[2][32], float alpha, int64_t row, int64_t col, int lane,
+                                            uint32_t& stores) {
+  if (col >= p.N) return;
   const bool inside = row < p.M;         // a box starts inside d or is not stored
-#pragma unroll 1
-  for (int c = 0; c < kCols; c += 64) {
-    uint32_t r[2][32];
-    tmem_ld_32x32b_x32(taddr + c, r[0]);
-    tmem_ld_32x32b_x32(taddr + c + 32, r[1]);
-    tmem_wait_ld32(r[0]);
-    tmem_wait_ld32(r[1]);
-    if (col + c + 64 > p.N && p.N % (p.out_f32 ? 4 : 8) != 0) {
-      if (row + lane < p.M) {
-        const int64_t at = (row + lane) * p.ldd + col + c;
+  if (col + 64 > p.N && p.N % (p.out_f32 ? 4 : 8) != 0) {
+    if (row + lane < p.M) {
+      const int64_t at = (row + lane) * p.ldd + col;
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {
-          if (col + c + j < p.N) {
-            const float v = __uint_as_float(r[j >> 5][j & 31]) * alpha;
-            if (p.out_f32)
-              static_cast<float*>(p.d)[at + j] = v;
-            else
-              static_cast<__nv_bfloat16*>(p.d)[at + j] = __float2bfloat16_rn(v);
-          }
+      for (int j = 0; j < 64; ++j) {
+        if (col + j < p.N) {
+          const float v = __uint_as_float(r[j >> 5][j & 31]) * alpha;
+          if (p.out_f32)
+            static_cast<float*>(p.d)[at + j] = v;
+          else
+            static_cast<__nv_bfloat16*>(p.d)[at + j] = __float2bfloat16_rn(v);
         }
       }
-      __syncwarp();
-    } else if (p.out_f32) {
+    }
+    __syncwarp();
+  } else if (p.out_f32) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint8_t* box = stg + (stores & 1) * 4096;
-        if (lane == 0) bulk_wait_group_read1();
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-              make_float4(__uint_as_float(r[h][4 * j]) * alpha, __uint_as_float(r[h][4 * j + 1]) * alpha,
-                          __uint_as_float(r[h][4 * j + 2]) * alpha, __uint_as_float(r[h][4 * j + 3]) * alpha);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          if (inside && col + c + 32 * h < p.N)
-            tma_store_2d(tm_d, box, static_cast<int>(col) + c + 32 * h, static_cast<int>(row));
-          bulk_commit_group();
-        }
-        ++stores;
-      }
-    } else {
+    for (int h = 0; h < 2; ++h) {
       uint8_t* box = stg + (stores & 1) * 4096;
       if (lane == 0) bulk_wait_group_read1();
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t* q = r[j >> 2] + 8 * (j & 3);
-        *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(
-            pack_bf16x2(__uint_as_float(q[0]) * alpha, __uint_as_float(q[1]) * alpha),
-            pack_bf16x2(__uint_as_float(q[2]) * alpha, __uint_as_float(q[3]) * alpha),
-            pack_bf16x2(__uint_as_float(q[4]) * alpha, __uint_as_float(q[5]) * alpha),
-            pack_bf16x2(__uint_as_float(q[6]) * alpha, __uint_as_float(q[7]) * alpha));
-      }
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+            make_float4(__uint_as_float(r[h][4 * j]) * alpha, __uint_as_float(r[h][4 * j + 1]) * alpha,
+                        __uint_as_float(r[h][4 * j + 2]) * alpha, __uint_as_float(r[h][4 * j + 3]) * alpha);
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
-        if (inside && col + c < p.N) tma_store_2d(tm_d, box, static_cast<int>(col) + c, static_cast<int>(row));
+        if (inside && col + 32 * h < p.N)
+          tma_store_2d(tm_d, box, static_cast<int>(col) + 32 * h, static_cast<int>(row));
         bulk_commit_group();
       }
       ++stores;
     }
+  } else {
+    uint8_t* box = stg + (stores & 1) * 4096;
+    if (lane == 0) bulk_wait_group_read1();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t* q = r[j >> 2] + 8 * (j & 3);
+      *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(
+          pack_bf16x2(__uint_as_float(q[0]) * alpha, __uint_as_float(q[1]) * alpha),
+          pack_bf16x2(__uint_as_float(q[2]) * alpha, __uint_as_float(q[3]) * alpha),
+          pack_bf16x2(__uint_as_float(q[4]) * alpha, __uint_as_float(q[5]) * alpha),
+          pack_bf16x2(__uint_as_float(q[6]) * alpha, __uint_as_float(q[7]) * alpha));
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (inside) tma_store_2d(tm_d, box, static_cast<int>(col), static_cast<int>(row));
+      bulk_commit_group();
+    }
+    ++stores;
   }
 }
 
@@ -319,8 +321,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       tc_fence_after_sync();
       const uint32_t taddr = lanes + acc.idx * BN;
       if constexpr (!kSwap) {
-        store_tile<BN>(p, &tm_d, stg, taddr, alpha, static_cast<int64_t>(mb) * 128 + quarter * 32,
-                       static_cast<int64_t>(nb) * BN, lane, stores);
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 64) {
+          uint32_t r[2][32];
+          load_chunk(taddr + c, r);
+          store_chunk(p, &tm_d, stg, r, alpha, static_cast<int64_t>(mb) * 128 + quarter * 32,
+                      static_cast<int64_t>(nb) * BN + c, lane, stores);
+        }
       } else {
         // The tile is D transposed: this lane is column n, TMEM columns are rows of D.
         const int64_t n = static_cast<int64_t>(mb) * 128 + quarter * 32 + lane;
@@ -360,6 +367,240 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Pair kernel: a cluster of two CTAs computes a 256 x 256 tile with
+// tcgen05.mma.cta_group::2.  Each CTA loads its own 128 rows of a and half of
+// the 256 rows of b, so a stage moves 32 KB of codes into each SM for 256 x 256 x
+// 256 products (the 1-CTA kernel moves 32 KB for 128 x 128 x 256), which is what
+// the SMs' share of L2 bandwidth asks for at the 4-bit rate; and, in its own
+// TMEM, holds its rows' sums, the scales of its rows of a and those of all 256
+// rows of b.
+//
+// TMEM: two accumulators of 256 columns and two sets of scale columns do not fit
+// 512 columns, so the accumulators overlap by kOverlap columns.  A tile's
+// epilogue drains those first and then lets the issuer start the next tile,
+// whose other columns were drained a tile earlier.
+namespace {
+
+template <bool kNv>
+struct MxPairCfg {
+  static constexpr int kAtoms = kNv ? 4 : 2;
+  static constexpr int kHalfBytes = 128 * 128;            // own rows of a, or own half of b
+  static constexpr int kSfBytes = kAtoms * kMx4AtomBytes; // of 128 rows
+  static constexpr int kStageBytes = 2 * kHalfBytes + 3 * kSfBytes;
+  static constexpr int kStages = 4;
+  static constexpr int kOutBytes = 8 * 2 * 4096;
+  static constexpr int kSetCols = 3 * kAtoms * 4;
+  static constexpr int kScaleCol = 512 - 2 * kSetCols;
+  static constexpr int kAcc1 = kScaleCol - 256;           // first column of the second accumulator
+  static constexpr int kOverlap = 256 - kAcc1;
+  static_assert(kOverlap <= 128, "an epilogue drains half of its columns before the next tile starts");
+  static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kOutBytes + static_cast<int>(sizeof(MxCtrl));
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+}  // namespace
+
+template <bool kNv>
+__global__ void __launch_bounds__(kMxPairThreads, 1)
+    gemm_mx4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                         const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
+                         const __grid_constant__ CUtensorMap tm_d, const Mx4Params p) {
+  using C = MxPairCfg<kNv>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem_out = smem + C::kStages * C::kStageBytes;
+  MxCtrl* ctrl = reinterpret_cast<MxCtrl*>(smem_out + C::kOutBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int num_mb = static_cast<int>((p.M + 255) / 256), num_nb = static_cast<int>((p.N + 255) / 256);
+  const int kblocks = static_cast<int>((p.K + kStageK - 1) / kStageK);
+  const int tiles = num_mb * num_nb;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&ctrl->full[s], 1);      // the leader's arrive + the bytes of both CTAs
+      mbar_init(&ctrl->empty[s], 1);     // the leader's MMA commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->sfree[b], 1);
+    }
+    mbar_init(&ctrl->tempty[0], 16);     // the epilogue warps of both CTAs: the overlap is drained
+    mbar_init(&ctrl->mma_done, 1);
+    mbar_init(&ctrl->never, 1);
+    ctrl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&ctrl->tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after_sync();
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const uint32_t tmem_base = ctrl->tmem_base;
+  volatile int* abort = &ctrl->abort;
+  const uint32_t peer_abort = mapa_shared(smem_addr(&ctrl->abort), rank ^ 1u);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_map(&tm_a);
+      tma_prefetch_map(&tm_b);
+      tma_prefetch_map(&tm_sa);
+      tma_prefetch_map(&tm_sb);
+      Ring<C::kStages> st;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < tiles; u += npairs) {
+        int mb, nb;
+        tile_coords(u, num_mb, num_nb, p.group_m, mb, nb);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait_bounded_pair(&ctrl->empty[st.idx], st.phase ^ 1u, abort, peer_abort, p.timeout_ns, p.err)) {
+            ok = false;
+            break;
+          }
+          uint8_t* stage = smem + st.idx * C::kStageBytes;
+          const uint32_t full = mapa_shared(smem_addr(&ctrl->full[st.idx]), 0);
+          if (leader) mbar_arrive_expect_tx(&ctrl->full[st.idx], 2 * C::kStageBytes);
+          tma_load_2d_pair(stage, &tm_a, full, kb * 128, mb * 256 + static_cast<int>(rank) * 128);
+          tma_load_2d_pair(stage + C::kHalfBytes, &tm_b, full, kb * 128, nb * 256 + static_cast<int>(rank) * 128);
+          tma_load_2d_pair(stage + 2 * C::kHalfBytes, &tm_sa, full, kb * C::kAtoms * 64, mb * 2 + static_cast<int>(rank));
+          tma_load_2d_pair(stage + 2 * C::kHalfBytes + C::kSfBytes, &tm_sb, full, kb * C::kAtoms * 64, nb * 2);
+          ++issued;
+          st.next();
+        }
+      }
+      if (leader) {
+        // The leader's full barriers count the bytes of both CTAs.
+        const int64_t first = issued > C::kStages ? issued - C::kStages : 0;
+        for (int64_t j = first; j < issued; ++j)
+          mbar_wait_bounded(&ctrl->full[j % C::kStages], static_cast<uint32_t>((j / C::kStages) & 1), nullptr,
+                            p.timeout_ns, p.err);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (of the leader CTA)
+    if (leader) {
+      const bool issuer = elect_one();
+      constexpr uint32_t idesc = idesc_mx4(256, 256, kNv);
+      const uint32_t smem0 = smem_addr(smem);
+      Ring<C::kStages> st;
+      Ring<2> acc, set;
+      uint32_t drained = 1;              // parity of the last tile's drain (the first tile waits for none)
+      bool ok = true;
+      if (p.inject_stall) ok = mbar_wait_bounded_pair(&ctrl->never, 0, abort, peer_abort, p.timeout_ns, p.err);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      for (int u = pair; ok && u < tiles; u += npairs) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded_pair<false>(&ctrl->tempty[0], drained, abort, peer_abort,
+                                                                   p.timeout_ns, p.err)))
+          break;
+        drained ^= 1u;
+        const uint32_t d_tmem = tmem_base + acc.idx * C::kAcc1;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          const bool got =
+              mbar_wait_bounded_pair<false>(&ctrl->full[st.idx], st.phase, abort, peer_abort, p.timeout_ns, p.err) &&
+              mbar_wait_bounded_pair<false>(&ctrl->sfree[set.idx], set.phase ^ 1u, abort, peer_abort, p.timeout_ns,
+                                            p.err);
+          if (!__all_sync(0xFFFFFFFFu, got)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a_addr = smem0 + st.idx * C::kStageBytes;
+          const uint64_t adesc = smem_desc_kmajor_sw128(a_addr);
+          const uint64_t bdesc = smem_desc_kmajor_sw128(a_addr + C::kHalfBytes);
+          const uint64_t sfdesc = smem_desc_atom(a_addr + 2 * C::kHalfBytes);
+          const uint32_t sfa = tmem_base + C::kScaleCol + set.idx * C::kSetCols, sfb = sfa + C::kAtoms * 4;
+          const int steps = static_cast<int>(min((p.K - static_cast<int64_t>(kb) * kStageK + 63) / 64, int64_t{4}));
+          if (issuer) {
+#pragma unroll
+            for (int i = 0; i < C::kAtoms; ++i) {
+              constexpr int kSf = C::kSfBytes >> 4, kAtom = kMx4AtomBytes >> 4;
+              tmem_cp_atom_pair(sfa + 4 * i, sfdesc + i * kAtom);
+              tmem_cp_atom_pair(sfb + 8 * i, sfdesc + kSf + i * kAtom);
+              tmem_cp_atom_pair(sfb + 8 * i + 4, sfdesc + 2 * kSf + i * kAtom);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k < steps) {
+                const int atom = kNv ? k : k >> 1;
+                umma_mx4_pair<kNv>(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc | idesc_scale_id(kNv ? 0 : 2 * (k & 1)),
+                                   sfa + 4 * atom, sfb + 8 * atom, (kb | k) != 0);
+              }
+            }
+            umma_commit_pair(&ctrl->empty[st.idx], 0x3);
+            umma_commit_pair(&ctrl->sfree[set.idx], 0x1);
+            if (kb == kblocks - 1) umma_commit_pair(&ctrl->tfull[acc.idx], 0x3);
+          }
+          __syncwarp();
+          st.next();
+          set.next();
+        }
+        acc.next();
+      }
+      if (issuer) umma_commit_pair(&ctrl->mma_done, 0x1);
+      __syncwarp();
+      mbar_wait_bounded(&ctrl->mma_done, 0, nullptr, p.timeout_ns, p.err);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ epilogue
+    // Two warpgroups: of each half of the columns a warp takes 64.
+    const int quarter = warp & 3, part = 64 * ((warp - kEpiWarp0) >> 2);
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint8_t* stg = smem_out + (warp - kEpiWarp0) * 8192;
+    const float alpha = (p.tsa ? __ldg(p.tsa) : 1.0f) * (p.tsb ? __ldg(p.tsb) : 1.0f);
+    const uint32_t tempty = mapa_shared(smem_addr(&ctrl->tempty[0]), 0);
+    Ring<2> acc;
+    uint32_t stores = 0;
+    for (int u = pair; u < tiles; u += npairs) {
+      int mb, nb;
+      tile_coords(u, num_mb, num_nb, p.group_m, mb, nb);
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded_pair<false>(&ctrl->tfull[acc.idx], acc.phase, abort, peer_abort,
+                                                                 p.timeout_ns, p.err)))
+        break;
+      tc_fence_after_sync();
+      const uint32_t taddr = lanes + acc.idx * C::kAcc1;
+      const int64_t row = static_cast<int64_t>(mb) * 256 + rank * 128 + quarter * 32, col = static_cast<int64_t>(nb) * 256;
+      // The half that overlaps the other accumulator first; once it is in
+      // registers the next tile may start.
+      const int first = (acc.idx == 0 ? 128 : 0) + part, second = first ^ 128;
+      uint32_t r[2][32];
+      load_chunk(taddr + first, r);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(&ctrl->tempty[0]);
+        else
+          mbar_arrive_remote(tempty);
+      }
+      store_chunk(p, &tm_d, stg, r, alpha, row, col + first, lane, stores);
+      load_chunk(taddr + second, r);
+      store_chunk(p, &tm_d, stg, r, alpha, row, col + second, lane, stores);
+      tc_fence_before_sync();
+      acc.next();
+    }
+    if (lane == 0) bulk_wait_group0();
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // every MMA of the pair is done and no signal is left in flight
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
@@ -432,10 +673,42 @@ cudaError_t launch_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
 }
 
 template <bool kNv>
+cudaError_t launch_mx4_pair(const Mx4GemmArgs& g, cudaStream_t stream) {
+  static PerContext<int> smem_set;
+  using C = MxPairCfg<kNv>;
+  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_pair_kernel<kNv>, C::kSmem); e != cudaSuccess) return e;
+  CUtensorMap ta, tb, tsa, tsb, td;
+  if (!codes_map(&ta, g.a, g.M, g.K, 128) || !codes_map(&tb, g.b, g.N, g.K, 128) ||
+      !scales_map(&tsa, g.sa, g.M, g.K, kNv, 1) || !scales_map(&tsb, g.sb, g.N, g.K, kNv, 2) || !mx_out_map(&td, g))
+    return cudaErrorInvalidValue;
+  const int64_t num_mb = (g.M + 255) / 256, tiles = num_mb * ((g.N + 255) / 256);
+  const Mx4Params p = mx_params(g, num_mb);
+  int64_t pairs = num_sms() / 2;
+  if (g.max_ctas > 1 && g.max_ctas / 2 < pairs) pairs = g.max_ctas / 2;
+  if (tiles < pairs) pairs = tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(kMxPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + set_pdl_attr(attr + 1, g.pdl);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_pair_kernel<kNv>, ta, tb, tsa, tsb, td, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool kNv>
 cudaError_t launch_mx4_fmt(const Mx4GemmArgs& g, cudaStream_t stream) {
   if (g.M <= 16) return launch_mx4<16, kNv, true>(g, stream);
   if (g.M <= 32) return launch_mx4<32, kNv, true>(g, stream);
   if (g.M <= 64) return launch_mx4<64, kNv, true>(g, stream);
+  const int64_t pair_tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
+  if (pair_tiles >= num_sms() / 2) return launch_mx4_pair<kNv>(g, stream);
   return launch_mx4<128, kNv, false>(g, stream);
 }
 

@@ -271,7 +271,7 @@ def test_captured_graph_on_a_side_stream():
     del graph
 
 
-@pytest.mark.parametrize("m", [4, 256])
+@pytest.mark.parametrize("m", [4, 256, 19000])
 def test_stalled_product_reports_timeout_and_recovers(m, monkeypatch):
     require_cuda()
     n, k = 256, 512
@@ -287,3 +287,18 @@ def test_stalled_product_reports_timeout_and_recovers(m, monkeypatch):
     d = fb.fp8blk_gemm_mx4(qa, sa, qb, sb, fb.NVFP4)
     assert fb.fp8blk_get_device_error() == 0
     _assert_product(d, a, b, 1.0, k, True, "after timeout")
+
+
+@pytest.mark.parametrize("m,n,k", [(2560, 2048, 512), (2500, 2100, 288), (256, 19000, 96)])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_large_product(m, n, k, fmt, out_dtype):
+    """Enough 256 x 256 tiles for every pair of SMs, the last ones cut in both directions and along K."""
+    require_cuda()
+    g = None if fmt == "mxfp4" else 0.02
+    (qa, sa), a = _operand(m, k, fmt, 1, g)
+    (qb, sb), b = _operand(n, k, fmt, 2, g)
+    d = fb.fp8blk_gemm_mx4(qa, sa, qb, sb, FORMATS[fmt], _scalar(g), _scalar(g), out_dtype=out_dtype)
+    assert fb.fp8blk_get_device_error() == 0
+    alpha = 1.0 if g is None else np.float64(np.float32(g) * np.float32(g))
+    _assert_product(d, a, b, alpha, k, out_dtype == torch.bfloat16, f"{m} {n} {k} {fmt}")
