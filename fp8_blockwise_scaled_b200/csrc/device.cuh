@@ -98,6 +98,32 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same wait for a role that usually waits only briefly: it polls without
+// the hint and reads the clock only after kHotPolls polls, since a read of
+// %globaltimer costs more than such a wait takes (the hand-over between two
+// tiles of the 4-bit GEMM lost ~450 cycles to it).  peer_abort 0: no other CTA to
+// tell.
+constexpr uint32_t kHotPolls = 256;
+
+__device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t peer_abort,
+                                              uint64_t timeout_ns, unsigned int* err) {
+  for (uint32_t it = 0; it < kHotPolls; ++it)
+    if (mbar_try_wait_nohint(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait_nohint(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (abort && *abort) return false;
+      if (global_timer_ns() - t0 > timeout_ns) {
+        if (abort) *abort = 1;
+        if (peer_abort) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_abort), "r"(1u) : "memory");
+        atomicOr(err, kErrTimeoutBit);
+        return false;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ TMA
 // 2-D tiled bulk tensor load global -> shared, completion counted in bytes on
 // `bar`.  (x, y) = (innermost, outer) element coordinates of the box.

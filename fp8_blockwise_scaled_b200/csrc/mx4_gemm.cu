@@ -9,16 +9,18 @@
 // atoms arrive by TMA next to the codes and are copied from shared memory to
 // TMEM by tcgen05.cp, in the order of the MMAs that read them.  Two sets of
 // scale columns alternate; a set is rewritten once the MMAs that read it have
-// completed (their commit).
+// completed (their commit).  Measured against it on 8192^3: four warps that
+// write the scales with tcgen05.st run MXFP4 equally fast (207 us) and NVFP4
+// slower (250 us instead of 222 us), copies of half the size one step ahead of
+// the MMAs 320 us.
 //
 // Warp roles (256 threads): warp 0 loads, warp 1 owns TMEM and issues copies
 // and MMAs, warps 4-7 drain the accumulators (two of them alternate, so a
 // tile's epilogue runs under the next tile's K loop).
 //
-// gemm_mx4_kernel: one CTA per SM, 128 x BN tiles.  kSwap exchanges the
-// operands' roles for few rows of a (decoding): 128 rows of b are the MMA's
-// M side and BN = 16 .. 128 rows of a its N side, so the tile is as high as the
-// weights are and hardly wider than the tokens.
+// gemm_mx4_kernel: persistent, one CTA per SM, 128 x 128 tiles.
+// gemm_mx4_pair_kernel: 256 x 256 tiles on pairs of SMs, for large outputs.
+// gemm_mx4_few_kernel: few rows of a (decoding), K split over a cluster.
 //
 // Every wait is bounded as in gemm.cu.
 #include <cudaTypedefs.h>
@@ -57,7 +59,7 @@ struct MxCfg {
   static constexpr int kBBytes = BN * 128;
   static constexpr int kSfBytes = kAtoms * kMx4AtomBytes;    // of each operand
   static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
-  static constexpr int kStages = BN == 128 ? 5 : (BN == 64 ? 6 : 8);
+  static constexpr int kStages = 5;
   static constexpr int kOutBytes = 4 * 2 * 4096;          // two 32-row boxes of 128 bytes for each epilogue warp
   static constexpr int kSetCols = 2 * kAtoms * 4;         // TMEM columns of one set of scales
   static constexpr int kTmemUsed = 2 * BN + 2 * kSetCols;
@@ -81,8 +83,10 @@ constexpr int mx_smem_bytes() {
   return 1024 + C::kStages * C::kStageBytes + C::kOutBytes + static_cast<int>(sizeof(MxCtrl));
 }
 
-__device__ __forceinline__ void bulk_wait_group_read1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+// Waits until the oldest of a thread's kBoxes staging boxes has been read by its store.
+template <int kBoxes>
+__device__ __forceinline__ void bulk_wait_box_free() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
 }
 
 // 64 columns of one warp's 32 accumulator rows.
@@ -94,11 +98,12 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[2][32])
 }
 
 // Those columns to d (row, col: the chunk's first): times alpha, rounded to bf16
-// (one box of 64 columns) or as fp32 (two boxes of 32), through the warp's two
-// staging boxes and TMA stores, which clip at d's last row and column.  A TMA
+// (one box of 64 columns) or as fp32 (two boxes of 32), through the warp's
+// kBoxes staging boxes and TMA stores, which clip at d's last row and column.  A TMA
 // store clips columns in units of 16 bytes: where N is no multiple of them, the
 // last columns are stored one by one, so that nothing behind column N is
 // written.  `stores`: boxes this warp has staged.
+template <int kBoxes>
 __device__ __forceinline__ void store_chunk(const Mx4Params& p, const CUtensorMap* tm_d, uint8_t* stg,
                                             const uint32_t (&r)[2][32], float alpha, int64_t row, int64_t col, int lane,
                                             uint32_t& stores) {
@@ -122,8 +127,8 @@ __device__ __forceinline__ void store_chunk(const Mx4Params& p, const CUtensorMa
   } else if (p.out_f32) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint8_t* box = stg + (stores & 1) * 4096;
-      if (lane == 0) bulk_wait_group_read1();
+      uint8_t* box = stg + (stores % kBoxes) * 4096;
+      if (lane == 0) bulk_wait_box_free<kBoxes>();
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -140,8 +145,8 @@ __device__ __forceinline__ void store_chunk(const Mx4Params& p, const CUtensorMa
       ++stores;
     }
   } else {
-    uint8_t* box = stg + (stores & 1) * 4096;
-    if (lane == 0) bulk_wait_group_read1();
+    uint8_t* box = stg + (stores % kBoxes) * 4096;
+    if (lane == 0) bulk_wait_box_free<kBoxes>();
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -164,7 +169,7 @@ __device__ __forceinline__ void store_chunk(const Mx4Params& p, const CUtensorMa
 
 }  // namespace
 
-template <int BN, bool kNv, bool kSwap>
+template <int BN, bool kNv>
 __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_mx4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                     const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
@@ -175,9 +180,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   uint8_t* smem_out = smem + C::kStages * C::kStageBytes;
   MxCtrl* ctrl = reinterpret_cast<MxCtrl*>(smem_out + C::kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // The MMA's M side in tiles of 128 rows, its N side in tiles of BN.
-  const int num_mb = static_cast<int>(((kSwap ? p.N : p.M) + 127) / 128);
-  const int num_nb = static_cast<int>(((kSwap ? p.M : p.N) + BN - 1) / BN);
+  const int num_mb = static_cast<int>((p.M + 127) / 128), num_nb = static_cast<int>((p.N + BN - 1) / BN);
   const int kblocks = static_cast<int>((p.K + kStageK - 1) / kStageK);
   const int tiles = num_mb * num_nb;
 
@@ -211,14 +214,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const CUtensorMap* ma = kSwap ? &tm_b : &tm_a;
-      const CUtensorMap* mb_ = kSwap ? &tm_a : &tm_b;
-      const CUtensorMap* msa = kSwap ? &tm_sb : &tm_sa;
-      const CUtensorMap* msb = kSwap ? &tm_sa : &tm_sb;
-      tma_prefetch_map(ma);
-      tma_prefetch_map(mb_);
-      tma_prefetch_map(msa);
-      tma_prefetch_map(msb);
+      tma_prefetch_map(&tm_a);
+      tma_prefetch_map(&tm_b);
+      tma_prefetch_map(&tm_sa);
+      tma_prefetch_map(&tm_sb);
       Ring<C::kStages> st;
       int64_t issued = 0;
       bool ok = true;
@@ -233,11 +232,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           uint8_t* stage = smem + st.idx * C::kStageBytes;
           uint64_t* full = &ctrl->full[st.idx];
           mbar_arrive_expect_tx(full, C::kStageBytes);
-          tma_load_2d(stage, ma, full, kb * 128, mb * 128);
-          tma_load_2d(stage + C::kABytes, mb_, full, kb * 128, nb * BN);
+          tma_load_2d(stage, &tm_a, full, kb * 128, mb * 128);
+          tma_load_2d(stage + C::kABytes, &tm_b, full, kb * 128, nb * BN);
           // Scale maps: rows of 128-row blocks, columns of 8-byte words, 64 to an atom.
-          tma_load_2d(stage + C::kABytes + C::kBBytes, msa, full, kb * C::kAtoms * 64, mb);
-          tma_load_2d(stage + C::kABytes + C::kBBytes + C::kSfBytes, msb, full, kb * C::kAtoms * 64, nb * BN / 128);
+          tma_load_2d(stage + C::kABytes + C::kBBytes, &tm_sa, full, kb * C::kAtoms * 64, mb);
+          tma_load_2d(stage + C::kABytes + C::kBBytes + C::kSfBytes, &tm_sb, full, kb * C::kAtoms * 64, nb * BN / 128);
           ++issued;
           st.next();
         }
@@ -259,12 +258,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     ok = __all_sync(0xFFFFFFFFu, ok);
     for (int u = blockIdx.x; ok && u < tiles; u += gridDim.x) {
       if (!__all_sync(0xFFFFFFFFu,
-                      mbar_wait_bounded<false>(&ctrl->tempty[acc.idx], acc.phase ^ 1u, abort, p.timeout_ns, p.err)))
+                      mbar_wait_hot(&ctrl->tempty[acc.idx], acc.phase ^ 1u, abort, 0, p.timeout_ns, p.err)))
         break;
       const uint32_t d_tmem = tmem_base + acc.idx * BN;
       for (int kb = 0; kb < kblocks; ++kb) {
-        const bool got = mbar_wait_bounded<false>(&ctrl->full[st.idx], st.phase, abort, p.timeout_ns, p.err) &&
-                         mbar_wait_bounded<false>(&ctrl->sfree[set.idx], set.phase ^ 1u, abort, p.timeout_ns, p.err);
+        const bool got = mbar_wait_hot(&ctrl->full[st.idx], st.phase, abort, 0, p.timeout_ns, p.err) &&
+                         mbar_wait_hot(&ctrl->sfree[set.idx], set.phase ^ 1u, abort, 0, p.timeout_ns, p.err);
         if (!__all_sync(0xFFFFFFFFu, got)) {
           ok = false;
           break;
@@ -316,49 +315,23 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       int mb, nb;
       tile_coords(u, num_mb, num_nb, p.group_m, mb, nb);
       if (!__all_sync(0xFFFFFFFFu,
-                      mbar_wait_bounded<false>(&ctrl->tfull[acc.idx], acc.phase, abort, p.timeout_ns, p.err)))
+                      mbar_wait_bounded(&ctrl->tfull[acc.idx], acc.phase, abort, p.timeout_ns, p.err)))
         break;
       tc_fence_after_sync();
       const uint32_t taddr = lanes + acc.idx * BN;
-      if constexpr (!kSwap) {
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 64) {
-          uint32_t r[2][32];
-          load_chunk(taddr + c, r);
-          store_chunk(p, &tm_d, stg, r, alpha, static_cast<int64_t>(mb) * 128 + quarter * 32,
-                      static_cast<int64_t>(nb) * BN + c, lane, stores);
-        }
-      } else {
-        // The tile is D transposed: this lane is column n, TMEM columns are rows of D.
-        const int64_t n = static_cast<int64_t>(mb) * 128 + quarter * 32 + lane;
-        const int64_t m0 = static_cast<int64_t>(nb) * BN;
-        const int rows = static_cast<int>(min(p.M - m0, static_cast<int64_t>(BN)));
-        for (int c = 0; c < rows; c += 16) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(taddr + c, r);
-          tmem_wait_ld16(r);
-          if (n < p.N) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              if (c + j < rows) {
-                const float v = __uint_as_float(r[j]) * alpha;
-                const int64_t at = (m0 + c + j) * p.ldd + n;
-                if (p.out_f32)
-                  static_cast<float*>(p.d)[at] = v;
-                else
-                  static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16_rn(v);
-              }
-            }
-          }
-          __syncwarp();
-        }
+      for (int c = 0; c < BN; c += 64) {
+        uint32_t r[2][32];
+        load_chunk(taddr + c, r);
+        store_chunk<2>(p, &tm_d, stg, r, alpha, static_cast<int64_t>(mb) * 128 + quarter * 32,
+                       static_cast<int64_t>(nb) * BN + c, lane, stores);
       }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->tempty[acc.idx]);
       acc.next();
     }
-    if (!kSwap && lane == 0) bulk_wait_group0();
+    if (lane == 0) bulk_wait_group0();
   }
 
   tc_fence_before_sync();
@@ -383,6 +356,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 // 512 columns, so the accumulators overlap by kOverlap columns.  A tile's
 // epilogue drains those first and then lets the issuer start the next tile,
 // whose other columns were drained a tile earlier.
+//
+// What bounds it: power.  A stage takes 735 (MXFP4) or 768 cycles (NVFP4) where
+// its MMAs alone take 512, but the SMs run at 1.6 GHz under it, and variants that
+// need fewer cycles ran at lower clocks for the same time.  8192^3: 206 us, 5.3
+// PFLOP/s (MXFP4), 222 us (NVFP4).  With K = 1536 another 1500 cycles a tile go
+// to the hand-over between tiles.
 namespace {
 
 template <bool kNv>
@@ -391,8 +370,8 @@ struct MxPairCfg {
   static constexpr int kHalfBytes = 128 * 128;            // own rows of a, or own half of b
   static constexpr int kSfBytes = kAtoms * kMx4AtomBytes; // of 128 rows
   static constexpr int kStageBytes = 2 * kHalfBytes + 3 * kSfBytes;
-  static constexpr int kStages = 4;
-  static constexpr int kOutBytes = 8 * 2 * 4096;
+  static constexpr int kStages = 5;
+  static constexpr int kOutBytes = 8 * 4096;              // one 32-row box of 128 bytes for each epilogue warp
   static constexpr int kSetCols = 3 * kAtoms * 4;
   static constexpr int kScaleCol = 512 - 2 * kSetCols;
   static constexpr int kAcc1 = kScaleCol - 256;           // first column of the second accumulator
@@ -502,15 +481,15 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
       if (p.inject_stall) ok = mbar_wait_bounded_pair(&ctrl->never, 0, abort, peer_abort, p.timeout_ns, p.err);
       ok = __all_sync(0xFFFFFFFFu, ok);
       for (int u = pair; ok && u < tiles; u += npairs) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded_pair<false>(&ctrl->tempty[0], drained, abort, peer_abort,
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_hot(&ctrl->tempty[0], drained, abort, peer_abort,
                                                                    p.timeout_ns, p.err)))
           break;
         drained ^= 1u;
         const uint32_t d_tmem = tmem_base + acc.idx * C::kAcc1;
         for (int kb = 0; kb < kblocks; ++kb) {
           const bool got =
-              mbar_wait_bounded_pair<false>(&ctrl->full[st.idx], st.phase, abort, peer_abort, p.timeout_ns, p.err) &&
-              mbar_wait_bounded_pair<false>(&ctrl->sfree[set.idx], set.phase ^ 1u, abort, peer_abort, p.timeout_ns,
+              mbar_wait_hot(&ctrl->full[st.idx], st.phase, abort, peer_abort, p.timeout_ns, p.err) &&
+              mbar_wait_hot(&ctrl->sfree[set.idx], set.phase ^ 1u, abort, peer_abort, p.timeout_ns,
                                             p.err);
           if (!__all_sync(0xFFFFFFFFu, got)) {
             ok = false;
@@ -558,7 +537,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     // Two warpgroups: of each half of the columns a warp takes 64.
     const int quarter = warp & 3, part = 64 * ((warp - kEpiWarp0) >> 2);
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint8_t* stg = smem_out + (warp - kEpiWarp0) * 8192;
+    uint8_t* stg = smem_out + (warp - kEpiWarp0) * 4096;
     const float alpha = (p.tsa ? __ldg(p.tsa) : 1.0f) * (p.tsb ? __ldg(p.tsb) : 1.0f);
     const uint32_t tempty = mapa_shared(smem_addr(&ctrl->tempty[0]), 0);
     Ring<2> acc;
@@ -566,7 +545,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     for (int u = pair; u < tiles; u += npairs) {
       int mb, nb;
       tile_coords(u, num_mb, num_nb, p.group_m, mb, nb);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded_pair<false>(&ctrl->tfull[acc.idx], acc.phase, abort, peer_abort,
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded_pair(&ctrl->tfull[acc.idx], acc.phase, abort, peer_abort,
                                                                  p.timeout_ns, p.err)))
         break;
       tc_fence_after_sync();
@@ -585,9 +564,9 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         else
           mbar_arrive_remote(tempty);
       }
-      store_chunk(p, &tm_d, stg, r, alpha, row, col + first, lane, stores);
+      store_chunk<1>(p, &tm_d, stg, r, alpha, row, col + first, lane, stores);
       load_chunk(taddr + second, r);
-      store_chunk(p, &tm_d, stg, r, alpha, row, col + second, lane, stores);
+      store_chunk<1>(p, &tm_d, stg, r, alpha, row, col + second, lane, stores);
       tc_fence_before_sync();
       acc.next();
     }
@@ -601,6 +580,210 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows of a (M <= BN = 16, 32 or 64: decoding).  The operands' roles are
+// exchanged: 128 rows of b are the MMA's M side and all rows of a its N side, so
+// the tile is D transposed and the work is one read of b.  That read is bound by
+// HBM where b is large and by latency where it is not, so the K loop of a tile is
+// split over the CTAs of a cluster (1 to 8): each sums its stages in TMEM and
+// leaves the fp32 partial tile in its shared memory; after a cluster barrier
+// each adds its share of the columns over the partials in the order of their
+// ranks (always the same sum) and stores it.  N = 1536, K = 8960, one row: 15.8 us
+// unsplit.
+namespace {
+
+template <int BN, bool kNv>
+struct FewCfg {
+  static constexpr int kAtoms = kNv ? 4 : 2;
+  static constexpr int kABytes = 128 * 128;               // b: the MMA's A operand
+  static constexpr int kBBytes = BN * 128;
+  static constexpr int kSfBytes = kAtoms * kMx4AtomBytes;
+  static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
+  static constexpr int kStages = BN == 64 ? 3 : 4;        // two CTAs per SM
+  static constexpr int kSetCols = 2 * kAtoms * 4;
+  static constexpr int kScaleCol = BN < 32 ? 32 : BN;
+  static constexpr int kTmemCols = 128;
+  static_assert(kScaleCol + 2 * kSetCols <= kTmemCols, "accumulator and two sets of scales");
+  static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+  static_assert(BN * 128 * 4 <= kStages * kStageBytes, "the partial tile takes the stages' place");
+};
+
+template <int BN, bool kNv>
+constexpr int few_smem_bytes() {
+  return 1024 + FewCfg<BN, kNv>::kStages * FewCfg<BN, kNv>::kStageBytes + static_cast<int>(sizeof(MxCtrl));
+}
+static_assert(2 * (few_smem_bytes<64, true>() + 1024) <= 227 * 1024 && 2 * (few_smem_bytes<32, true>() + 1024) <= 227 * 1024,
+              "two CTAs per SM");
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+}  // namespace
+
+template <int BN, bool kNv>
+__global__ void __launch_bounds__(kMxThreads, 2)
+    gemm_mx4_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                        const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
+                        const Mx4Params p, int splits) {
+  using C = FewCfg<BN, kNv>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  MxCtrl* ctrl = reinterpret_cast<MxCtrl*>(smem + C::kStages * C::kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = static_cast<int>(blockIdx.x) / splits, rank = static_cast<int>(blockIdx.x) - tile * splits;
+  const int64_t all = (p.K + kStageK - 1) / kStageK;
+  const int kb0 = static_cast<int>(rank * all / splits), kb1 = static_cast<int>((rank + 1) * all / splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) mbar_init(&ctrl->sfree[b], 1);
+    mbar_init(&ctrl->mma_done, 1);
+    mbar_init(&ctrl->never, 1);
+    ctrl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctrl->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const uint32_t tmem_base = ctrl->tmem_base;
+  volatile int* abort = &ctrl->abort;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int issued = 0;
+      Ring<C::kStages> st;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(&ctrl->empty[st.idx], st.phase ^ 1u, abort, p.timeout_ns, p.err)) break;
+        uint8_t* stage = smem + st.idx * C::kStageBytes;
+        uint64_t* full = &ctrl->full[st.idx];
+        mbar_arrive_expect_tx(full, C::kStageBytes);
+        tma_load_2d(stage, &tm_b, full, kb * 128, tile * 128);
+        tma_load_2d(stage + C::kABytes, &tm_a, full, kb * 128, 0);
+        tma_load_2d(stage + C::kABytes + C::kBBytes, &tm_sb, full, kb * C::kAtoms * 64, tile);
+        tma_load_2d(stage + C::kABytes + C::kBBytes + C::kSfBytes, &tm_sa, full, kb * C::kAtoms * 64, 0);
+        ++issued;
+        st.next();
+      }
+      for (int j = issued > C::kStages ? issued - C::kStages : 0; j < issued; ++j)
+        mbar_wait_bounded(&ctrl->full[j % C::kStages], static_cast<uint32_t>((j / C::kStages) & 1), nullptr,
+                          p.timeout_ns, p.err);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = idesc_mx4(128, BN, kNv);
+    const uint32_t smem0 = smem_addr(smem);
+    Ring<C::kStages> st;
+    Ring<2> set;
+    bool ok = true;
+    if (p.inject_stall) ok = mbar_wait_bounded(&ctrl->never, 0, abort, p.timeout_ns, p.err);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    for (int kb = kb0; ok && kb < kb1; ++kb) {
+      const bool got = mbar_wait_hot(&ctrl->full[st.idx], st.phase, abort, 0, p.timeout_ns, p.err) &&
+                       mbar_wait_hot(&ctrl->sfree[set.idx], set.phase ^ 1u, abort, 0, p.timeout_ns, p.err);
+      ok = __all_sync(0xFFFFFFFFu, got);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t a_addr = smem0 + st.idx * C::kStageBytes;
+      const uint64_t adesc = smem_desc_kmajor_sw128(a_addr), bdesc = smem_desc_kmajor_sw128(a_addr + C::kABytes);
+      const uint64_t sfdesc = smem_desc_atom(a_addr + C::kABytes + C::kBBytes);
+      const uint32_t sfa = tmem_base + C::kScaleCol + set.idx * C::kSetCols, sfb = sfa + C::kAtoms * 4;
+      const int steps = static_cast<int>(min((p.K - static_cast<int64_t>(kb) * kStageK + 63) / 64, int64_t{4}));
+      if (leader) {
+#pragma unroll
+        for (int i = 0; i < C::kAtoms; ++i) {
+          tmem_cp_atom(sfa + 4 * i, sfdesc + i * (kMx4AtomBytes >> 4));
+          tmem_cp_atom(sfb + 4 * i, sfdesc + ((C::kSfBytes + i * kMx4AtomBytes) >> 4));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < steps) {
+            const int atom = kNv ? k : k >> 1;
+            umma_mx4<kNv>(tmem_base, adesc + 2 * k, bdesc + 2 * k, idesc | idesc_scale_id(kNv ? 0 : 2 * (k & 1)),
+                          sfa + 4 * atom, sfb + 4 * atom, (kb != kb0) | (k != 0));
+          }
+        }
+        umma_commit(&ctrl->empty[st.idx]);
+        umma_commit(&ctrl->sfree[set.idx]);
+      }
+      __syncwarp();
+      st.next();
+      set.next();
+    }
+    if (leader) umma_commit(&ctrl->mma_done);
+    __syncwarp();
+    // The partial tile takes the stages' place: only when every stage has arrived and been read.
+    if (!mbar_wait_bounded(&ctrl->mma_done, 0, nullptr, p.timeout_ns, p.err) || !ok) *abort = 1;
+  }
+  tc_fence_before_sync();
+  __syncthreads();                       // the sums are complete (or a role gave up)
+  const bool done = *abort == 0;
+  const int rows = static_cast<int>(p.M);
+  float* part = reinterpret_cast<float*>(smem);   // [rows][128]
+  if (done && warp >= kEpiWarp0) {
+    tc_fence_after_sync();
+    const int quarter = warp & 3;
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    for (int c = 0; c < rows; c += 16) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(lanes + c, r);
+      tmem_wait_ld16(r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c + j < rows) part[(c + j) * 128 + quarter * 32 + lane] = __uint_as_float(r[j]);
+    }
+  }
+  tc_fence_before_sync();
+  if (splits > 1) {
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  // Column n of the tile: this CTA's share is 128 / splits of them.
+  if (done) {
+    const float alpha = (p.tsa ? __ldg(p.tsa) : 1.0f) * (p.tsb ? __ldg(p.tsb) : 1.0f);
+    const int share = 128 / splits;
+    const uint32_t part0 = smem_addr(part);
+    for (int i = threadIdx.x; i < rows * share; i += kMxThreads) {
+      const int m = i / share, n = rank * share + (i - m * share);
+      const uint32_t at = part0 + static_cast<uint32_t>(m * 128 + n) * 4;
+      float sum = 0.0f;
+      if (splits > 1) {
+        for (int s = 0; s < splits; ++s) sum += ld_shared_cluster_f32(mapa_shared(at, s));
+      } else {
+        sum = part[m * 128 + n];
+      }
+      const int64_t col = static_cast<int64_t>(tile) * 128 + n;
+      if (col < p.N) {
+        const float v = sum * alpha;
+        if (p.out_f32)
+          static_cast<float*>(p.d)[m * p.ldd + col] = v;
+        else
+          static_cast<__nv_bfloat16*>(p.d)[m * p.ldd + col] = __float2bfloat16_rn(v);
+      }
+    }
+  }
+  if (splits > 1) cluster_sync();        // no CTA leaves while its partials are read
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, C::kTmemCols);
   }
 }
 
@@ -645,17 +828,17 @@ Mx4Params mx_params(const Mx4GemmArgs& g, int64_t num_mb) {
   return p;
 }
 
-template <int BN, bool kNv, bool kSwap>
+template <int BN, bool kNv>
 cudaError_t launch_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
   static PerContext<int> smem_set;
   constexpr int kSmem = mx_smem_bytes<BN, kNv>();
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_kernel<BN, kNv, kSwap>, kSmem); e != cudaSuccess) return e;
+  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_kernel<BN, kNv>, kSmem); e != cudaSuccess) return e;
   CUtensorMap ta, tb, tsa, tsb, td;
-  if (!codes_map(&ta, g.a, g.M, g.K, kSwap ? BN : 128) || !codes_map(&tb, g.b, g.N, g.K, kSwap ? 128 : BN) ||
+  if (!codes_map(&ta, g.a, g.M, g.K, 128) || !codes_map(&tb, g.b, g.N, g.K, BN) ||
       !scales_map(&tsa, g.sa, g.M, g.K, kNv, 1) || !scales_map(&tsb, g.sb, g.N, g.K, kNv, 1) || !mx_out_map(&td, g))
     return cudaErrorInvalidValue;
-  const int64_t num_mb = ((kSwap ? g.N : g.M) + 127) / 128, num_nb = ((kSwap ? g.M : g.N) + BN - 1) / BN;
+  const int64_t num_mb = (g.M + 127) / 128, num_nb = (g.N + BN - 1) / BN;
   const Mx4Params p = mx_params(g, num_mb);
   int64_t ctas = num_sms();
   if (g.max_ctas > 0 && g.max_ctas < ctas) ctas = g.max_ctas;
@@ -668,7 +851,39 @@ cudaError_t launch_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   cfg.numAttrs = set_pdl_attr(attr, g.pdl);
   cfg.attrs = attr;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<BN, kNv, kSwap>, ta, tb, tsa, tsb, td, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<BN, kNv>, ta, tb, tsa, tsb, td, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int BN, bool kNv>
+cudaError_t launch_mx4_few(const Mx4GemmArgs& g, cudaStream_t stream) {
+  static PerContext<int> smem_set;
+  constexpr int kSmem = few_smem_bytes<BN, kNv>();
+  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_few_kernel<BN, kNv>, kSmem); e != cudaSuccess) return e;
+  CUtensorMap ta, tb, tsa, tsb;
+  if (!codes_map(&ta, g.a, g.M, g.K, BN) || !codes_map(&tb, g.b, g.N, g.K, 128) ||
+      !scales_map(&tsa, g.sa, g.M, g.K, kNv, 1) || !scales_map(&tsb, g.sb, g.N, g.K, kNv, 1))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = (g.N + 127) / 128, kblocks = (g.K + kStageK - 1) / kStageK;
+  // As many CTAs as the SMs hold (two each), every one with at least two stages.
+  int splits = 1;
+  while (splits < 8 && 2 * splits * tiles <= 2 * num_sms() && kblocks >= 4 * splits) splits *= 2;
+  // It is not persistent: a cap on the CTAs is kept by the 1-CTA kernel.
+  if (g.max_ctas > 0 && tiles * splits > g.max_ctas) return launch_mx4<128, kNv>(g, stream);
+  const Mx4Params p = mx_params(g, 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), 1, 1);
+  cfg.blockDim = dim3(kMxThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + set_pdl_attr(attr + 1, g.pdl);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_few_kernel<BN, kNv>, ta, tb, tsa, tsb, p, splits);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -704,12 +919,12 @@ cudaError_t launch_mx4_pair(const Mx4GemmArgs& g, cudaStream_t stream) {
 
 template <bool kNv>
 cudaError_t launch_mx4_fmt(const Mx4GemmArgs& g, cudaStream_t stream) {
-  if (g.M <= 16) return launch_mx4<16, kNv, true>(g, stream);
-  if (g.M <= 32) return launch_mx4<32, kNv, true>(g, stream);
-  if (g.M <= 64) return launch_mx4<64, kNv, true>(g, stream);
+  if (g.M <= 16) return launch_mx4_few<16, kNv>(g, stream);
+  if (g.M <= 32) return launch_mx4_few<32, kNv>(g, stream);
+  if (g.M <= 64) return launch_mx4_few<64, kNv>(g, stream);
   const int64_t pair_tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
   if (pair_tiles >= num_sms() / 2) return launch_mx4_pair<kNv>(g, stream);
-  return launch_mx4<128, kNv, false>(g, stream);
+  return launch_mx4<128, kNv>(g, stream);
 }
 
 }  // namespace

@@ -153,7 +153,8 @@ def _assert_product(d, a, b, alpha, k, bf16, what):
 
 
 GEMM_SHAPES = [(1, 1, 32), (1, 200, 96), (5, 136, 512), (16, 128, 256), (17, 300, 224), (33, 129, 1504), (64, 64, 64),
-               (65, 72, 320), (128, 128, 256), (130, 264, 544), (257, 520, 800), (384, 1000, 1536), (700, 131, 288)]
+               (65, 72, 320), (128, 128, 256), (130, 264, 544), (257, 520, 800), (384, 1000, 1536), (700, 131, 288),
+               (2, 264, 4128), (20, 130, 2592), (50, 1000, 8960), (64, 4000, 1056)]
 
 
 @pytest.mark.parametrize("m,n,k", GEMM_SHAPES)
