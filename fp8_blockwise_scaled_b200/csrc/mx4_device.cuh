@@ -39,6 +39,17 @@ __device__ __forceinline__ uint32_t cvt8_e2m1(const float (&x)[8]) {
   return r;
 }
 
+// Two values -> two codes in the low byte, x0 in the low nibble.
+__device__ __forceinline__ uint32_t cvt2_e2m1(float x0, float x1) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
+      "cvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(x0), "f"(x1));
+  return r;
+}
+
 // One value -> its E4M3 code (saturating), and an E4M3 code's value.
 __device__ __forceinline__ uint32_t cvt_e4m3(float x) {
   uint16_t r;

@@ -50,11 +50,17 @@ struct Mx4Ctrl {
 constexpr int kSmem = 1024 + kStages * static_cast<int>(kTileBytes) + static_cast<int>(sizeof(Mx4Ctrl));
 static_assert(2 * (kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
 
-// Scale byte of a block of maximum amax, and what its values are divided by.
+// Scale byte of a block of maximum amax, and what its values are divided by.  g
+// and rg = RN(1 / g): the tensor's scale.  Both quotients are correctly rounded
+// by Markstein's correction, as x / s in qmath.cuh: q0 = RN(a y) with y the
+// correctly rounded reciprocal, then RN(q0 + RN(a - q0 b) y).
 template <bool kNv>
-__device__ __forceinline__ uint32_t block_scale(float amax, float g, QScale& q) {
+__device__ __forceinline__ uint32_t block_scale(float amax, float g, float rg, QScale& q) {
   if constexpr (kNv) {
-    const uint32_t byte = cvt_e4m3(__fdiv_rn(__fdiv_rn(amax, 6.0f), g));
+    constexpr float kSixth = 0x1.555556p-3f;              // RN(1 / 6)
+    const float a0 = amax * kSixth, a = fmaf(fmaf(-6.0f, a0, amax), kSixth, a0);
+    const float t0 = a * rg, t = fmaf(fmaf(-g, t0, a), rg, t0);
+    const uint32_t byte = cvt_e4m3(t);
     q.s = e4m3_value(byte) * g;
     q.nr = q.s > 0.0f ? -__frcp_rn(q.s) : 0.0f;
     return byte;
@@ -66,22 +72,13 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float g, QScale& q) 
   }
 }
 
-// Eight values of one block (or of eight, one each) -> eight codes.
+// A pair of values by their blocks' scales: -RN(x / d) (NVFP4, whose code signs
+// are flipped afterwards) or x / scale (MXFP4, exact).
 template <bool kNv>
-__device__ __forceinline__ uint32_t codes8(const float (&x)[8], const QScale& q) {
-  float w[8];
-  if constexpr (kNv) {
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) neg_quotient2(w[j], w[j + 1], x[j], x[j + 1], q.s, q.nr);
-    return cvt8_e2m1(w) ^ 0x88888888u;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = x[j] * q.nr;
-    return cvt8_e2m1(w);
-  }
+__device__ __forceinline__ float2 scaled2(float2 x, float2 s, float2 nr) {
+  if constexpr (kNv) return neg_quotient2(x, s, nr);
+  else return __fmul2_rn(x, nr);
 }
-
-__device__ __forceinline__ float half_max(uint32_t m) { return __uint_as_float(max(m << 16, m & 0xFFFF0000u)); }
 
 }  // namespace
 
@@ -117,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
   __syncthreads();
   griddep_wait();
   if (t == 0) griddep_launch_dependents();
-  const float g = kNv && a.tensor_scale ? __ldg(a.tensor_scale) : 1.0f;
+  const float g = kNv && a.tensor_scale ? __ldg(a.tensor_scale) : 1.0f, rg = __frcp_rn(g);
 
   // This thread's 8 x 8: rows 32 (warp / 2) + 8 (lane / 8) .., columns 64 (warp % 2) + 8 (lane % 8) ..
   const int r0 = 32 * (warp >> 1) + 8 * (lane >> 3), bj = lane & 7, c0 = 64 * (warp & 1) + 8 * bj;
@@ -146,39 +143,38 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
       }
     }
 
-    if constexpr (kRow) {
-      uint8_t* atoms = ctrl->atoms;
+    // Maxima of |x| on raw bits, two to a word: rm[p] rows 2p and 2p + 1 over this
+    // thread's 8 columns, cm[j] columns 2j and 2j + 1 over its 8 rows; then over
+    // the lanes that share the blocks.
+    [[maybe_unused]] uint32_t rm[4], cm[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const uint4 w = v[r];
-        uint32_t m = __vmaxu2(__vmaxu2(w.x & kAbs2, w.y & kAbs2), __vmaxu2(w.z & kAbs2, w.w & kAbs2));
-        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        if constexpr (!kNv) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        QScale q;
-        const uint32_t byte = block_scale<kNv>(half_max(m), g, q);
-        // 64 columns of the warp: one atom's four blocks (NVFP4), or two of an atom's (MXFP4).
-        if ((lane & (kNv ? 1 : 3)) == 0) {
-          const int row = r0 + r, atom = kNv ? warp & 1 : 0, j = kNv ? bj >> 1 : 2 * (warp & 1) + (bj >> 2);
-          atoms[atom * kMx4AtomBytes + (row & 31) * 16 + (row >> 5) * 4 + j] = static_cast<uint8_t>(byte);
+    for (int p = 0; p < 4; ++p) {
+      uint32_t m[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 w = v[2 * p + h];
+        const uint32_t a0 = w.x & kAbs2, a1 = w.y & kAbs2, a2 = w.z & kAbs2, a3 = w.w & kAbs2;
+        if constexpr (kRow) m[h] = __vmaxu2(__vmaxu2(a0, a1), __vmaxu2(a2, a3));
+        if constexpr (kColT) {
+          cm[0] = __vmaxu2(cm[0], a0);
+          cm[1] = __vmaxu2(cm[1], a1);
+          cm[2] = __vmaxu2(cm[2], a2);
+          cm[3] = __vmaxu2(cm[3], a3);
         }
-        float x[8];
-        unpack8(w, x);
-        const uint32_t code = codes8<kNv>(x, q);
-        if (row0 + r0 + r < a.rows && col0 + c0 < a.cols)
-          *reinterpret_cast<uint32_t*>(a.q_row + (row0 + r0 + r) * (a.cols / 2) + (col0 + c0) / 2) = code;
+      }
+      if constexpr (kRow) {
+        uint32_t k = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+        k = __vmaxu2(k, __shfl_xor_sync(0xFFFFFFFFu, k, 1));
+        if constexpr (!kNv) k = __vmaxu2(k, __shfl_xor_sync(0xFFFFFFFFu, k, 2));
+        rm[p] = k;
       }
     }
+
+    // Column scales.  NVFP4: lanes 8 apart share their 8 blocks; each computes those
+    // of one parity and hands them over.
+    [[maybe_unused]] float cs[8], cn[8];
     if constexpr (kColT) {
       uint8_t* atoms = ctrl->atoms_t;
-      uint8_t* lines = ctrl->codes_t;
-      uint32_t cm[4] = {0, 0, 0, 0};       // column maxima over this thread's 8 rows, two columns a word
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        cm[0] = __vmaxu2(cm[0], v[r].x & kAbs2);
-        cm[1] = __vmaxu2(cm[1], v[r].y & kAbs2);
-        cm[2] = __vmaxu2(cm[2], v[r].z & kAbs2);
-        cm[3] = __vmaxu2(cm[3], v[r].w & kAbs2);
-      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         cm[j] = __vmaxu2(cm[j], __shfl_xor_sync(0xFFFFFFFFu, cm[j], 8));
@@ -186,25 +182,105 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
       }
       // 32 rows of the warp: block warp / 2 of the one atom (MXFP4), or blocks 2 (warp / 2) and the next of eight.
       const int block = kNv ? 2 * (warp >> 1) + (lane >> 4) : warp >> 1;
-      const bool writes = kNv ? (lane & 8) == 0 : (lane & 24) == 0;
+      auto put = [&](int col, uint32_t byte) {
+        atoms[(block >> 2) * kMx4AtomBytes + (col & 31) * 16 + (col >> 5) * 4 + (block & 3)] = static_cast<uint8_t>(byte);
+      };
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t m = cm[c >> 1];
-        QScale q;
-        const uint32_t byte = block_scale<kNv>(__uint_as_float(c & 1 ? m & 0xFFFF0000u : m << 16), g, q);
-        const int col = c0 + c;
-        if (writes)
-          atoms[(block >> 2) * kMx4AtomBytes + (col & 31) * 16 + (col >> 5) * 4 + (block & 3)] = static_cast<uint8_t>(byte);
-        float x[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const uint32_t w = (c >> 1) == 0 ? v[r].x : (c >> 1) == 1 ? v[r].y : (c >> 1) == 2 ? v[r].z : v[r].w;
-          x[r] = c & 1 ? bf16hi(w) : bf16lo(w);
+      for (int j = 0; j < 4; ++j) {
+        const float lo = __uint_as_float(cm[j] << 16), hi = __uint_as_float(cm[j] & 0xFFFF0000u);
+        if constexpr (kNv) {
+          const bool odd = lane & 8;
+          QScale q;
+          put(c0 + 2 * j + odd, block_scale<kNv>(odd ? hi : lo, g, rg, q));
+          const float os = __shfl_xor_sync(0xFFFFFFFFu, q.s, 8), on = __shfl_xor_sync(0xFFFFFFFFu, q.nr, 8);
+          cs[2 * j] = odd ? os : q.s;
+          cs[2 * j + 1] = odd ? q.s : os;
+          cn[2 * j] = odd ? on : q.nr;
+          cn[2 * j + 1] = odd ? q.nr : on;
+        } else {
+          QScale q0, q1;
+          const uint32_t b0 = block_scale<kNv>(lo, g, rg, q0), b1 = block_scale<kNv>(hi, g, rg, q1);
+          if ((lane & 24) == 0) {
+            put(c0 + 2 * j, b0);
+            put(c0 + 2 * j + 1, b1);
+          }
+          cn[2 * j] = q0.nr;
+          cn[2 * j + 1] = q1.nr;
+          cs[2 * j] = cs[2 * j + 1] = 0.0f;
         }
-        // Line col, 4-byte unit r0 / 8; the line's 16-byte chunk r0 / 32 goes to chunk (r0 / 32) ^ (bj % 4).
-        *reinterpret_cast<uint32_t*>(lines + col * 64 + (((warp >> 1) ^ (bj & 3)) << 4) + ((lane >> 3) << 2)) =
-            codes8<kNv>(x, q);
       }
+    }
+
+    // Codes, two rows at a time: a column's values of rows 2p and 2p + 1 form one
+    // pair, divided in one packed step by the rows' scales and by the column's.
+    [[maybe_unused]] uint32_t line[8] = {0, 0, 0, 0, 0, 0, 0, 0};   // transposed: this thread's 8 rows of each column
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      float2 x[8];
+      {
+        const uint4 a0 = v[2 * p], a1 = v[2 * p + 1];
+        x[0] = make_float2(bf16lo(a0.x), bf16lo(a1.x));
+        x[1] = make_float2(bf16hi(a0.x), bf16hi(a1.x));
+        x[2] = make_float2(bf16lo(a0.y), bf16lo(a1.y));
+        x[3] = make_float2(bf16hi(a0.y), bf16hi(a1.y));
+        x[4] = make_float2(bf16lo(a0.z), bf16lo(a1.z));
+        x[5] = make_float2(bf16hi(a0.z), bf16hi(a1.z));
+        x[6] = make_float2(bf16lo(a0.w), bf16lo(a1.w));
+        x[7] = make_float2(bf16hi(a0.w), bf16hi(a1.w));
+      }
+      if constexpr (kRow) {
+        // 64 columns of the warp: one atom's four blocks (NVFP4), or two of an atom's (MXFP4).
+        auto put = [&](int row, uint32_t byte) {
+          const int atom = kNv ? warp & 1 : 0, j = kNv ? bj >> 1 : 2 * (warp & 1) + (bj >> 2);
+          ctrl->atoms[atom * kMx4AtomBytes + (row & 31) * 16 + (row >> 5) * 4 + j] = static_cast<uint8_t>(byte);
+        };
+        const float lo = __uint_as_float(rm[p] << 16), hi = __uint_as_float(rm[p] & 0xFFFF0000u);
+        float2 s2, nr2;
+        if constexpr (kNv) {               // neighbouring lanes share the two rows' blocks: one row each
+          const bool odd = lane & 1;
+          QScale q;
+          put(r0 + 2 * p + odd, block_scale<kNv>(odd ? hi : lo, g, rg, q));
+          const float os = __shfl_xor_sync(0xFFFFFFFFu, q.s, 1), on = __shfl_xor_sync(0xFFFFFFFFu, q.nr, 1);
+          s2 = odd ? make_float2(os, q.s) : make_float2(q.s, os);
+          nr2 = odd ? make_float2(on, q.nr) : make_float2(q.nr, on);
+        } else {
+          QScale q0, q1;
+          const uint32_t b0 = block_scale<kNv>(lo, g, rg, q0), b1 = block_scale<kNv>(hi, g, rg, q1);
+          if ((lane & 3) == 0) {
+            put(r0 + 2 * p, b0);
+            put(r0 + 2 * p + 1, b1);
+          }
+          s2 = make_float2(0.0f, 0.0f);
+          nr2 = make_float2(q0.nr, q1.nr);
+        }
+        float lo8[8], hi8[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float2 w = scaled2<kNv>(x[c], s2, nr2);
+          lo8[c] = w.x;
+          hi8[c] = w.y;
+        }
+        const int64_t row = row0 + r0 + 2 * p;
+        uint8_t* dst = a.q_row + row * (a.cols / 2) + (col0 + c0) / 2;
+        if (col0 + c0 < a.cols) {
+          if (row < a.rows) *reinterpret_cast<uint32_t*>(dst) = cvt8_e2m1(lo8) ^ (kNv ? 0x88888888u : 0u);
+          if (row + 1 < a.rows) *reinterpret_cast<uint32_t*>(dst + a.cols / 2) = cvt8_e2m1(hi8) ^ (kNv ? 0x88888888u : 0u);
+        }
+      }
+      if constexpr (kColT) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float2 w = scaled2<kNv>(x[c], make_float2(cs[c], cs[c]), make_float2(cn[c], cn[c]));
+          line[c] |= cvt2_e2m1(w.x, w.y) << (8 * p);
+        }
+      }
+    }
+    if constexpr (kColT) {
+      // Line c0 + c, 4-byte unit r0 / 8; the line's 16-byte chunk r0 / 32 goes to chunk (r0 / 32) ^ (bj % 4).
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint32_t*>(ctrl->codes_t + (c0 + c) * 64 + (((warp >> 1) ^ (bj & 3)) << 4) +
+                                     ((lane >> 3) << 2)) = line[c] ^ (kNv ? 0x88888888u : 0u);
     }
     __syncthreads();                       // the staged scales and lines are complete
     if constexpr (kRow) {
@@ -238,9 +314,12 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
   }
 }
 
-// Eight codes to eight bf16 values a thread: y = bf16(fl32(code * d)), d the
-// block's scale (times the tensor's, in fp32).  HBM bound: 1/2 + 1/32 or 1/16 B
-// read and 2 B written per element.
+// Codes to bf16 values: y = bf16(fl32(code * d)), d the block's scale (times the
+// tensor's, in fp32).  HBM bound: 1/2 + 1/32 or 1/16 B read and 2 B written per
+// element.  A block covers 32 rows x 256 columns, a thread 8 columns of four rows,
+// whose loads are all in flight together.
+constexpr int kDequantRows = 4;          // rows of a thread, 8 apart
+
 template <bool kNv>
 __global__ void __launch_bounds__(256) mx4_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                           const float* __restrict__ tensor_scale, int64_t rows,
@@ -249,33 +328,44 @@ __global__ void __launch_bounds__(256) mx4_dequant_kernel(const uint8_t* __restr
   if (threadIdx.x == 0) griddep_launch_dependents();
   const float g = kNv && tensor_scale ? __ldg(tensor_scale) : 1.0f;
   const int64_t atoms_k = (cols + mx4_atom_elems<kNv>() - 1) / mx4_atom_elems<kNv>();
-  const int64_t row = blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y;
+  const int64_t row0 = blockIdx.x * static_cast<int64_t>(8 * kDequantRows) + threadIdx.y;
   const int64_t col = 8 * (blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x);
-  if (row >= rows || col >= cols) return;
-  const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(q + (row * cols + col) / 2));
+  if (col >= cols) return;
   const int64_t block = col / mx4_block<kNv>();
-  const uint32_t byte = __ldg(s + ((row / 128) * atoms_k + block / 4) * kMx4AtomBytes + (row & 31) * 16 +
-                              ((row >> 5) & 3) * 4 + (block & 3));
-  const float d = kNv ? e4m3_value(byte) * g : e8m0_value(byte);
-  uint32_t h[4];                           // eight f16 values (exact)
-  asm("{\n\t.reg .b8 a, b, c, e;\n\t"
-      "mov.b32 {a, b, c, e}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, e;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(code));
-  uint32_t out[4];
+  uint32_t code[kDequantRows], byte[kDequantRows];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h[i]));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[i]) : "f"(hi * d), "f"(lo * d));
+  for (int i = 0; i < kDequantRows; ++i) {
+    const int64_t row = row0 + 8 * i;
+    if (row >= rows) break;
+    code[i] = __ldg(reinterpret_cast<const uint32_t*>(q + (row * cols + col) / 2));
+    byte[i] = __ldg(s + ((row / 128) * atoms_k + block / 4) * kMx4AtomBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
+                    (block & 3));
   }
-  *reinterpret_cast<uint4*>(y + row * ldy + col) = make_uint4(out[0], out[1], out[2], out[3]);
+#pragma unroll
+  for (int i = 0; i < kDequantRows; ++i) {
+    const int64_t row = row0 + 8 * i;
+    if (row >= rows) break;
+    const float d = kNv ? e4m3_value(byte[i]) * g : e8m0_value(byte[i]);
+    uint32_t h[4];                         // eight f16 values (exact)
+    asm("{\n\t.reg .b8 a, b, c, e;\n\t"
+        "mov.b32 {a, b, c, e}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, e;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(code[i]));
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+          : "=f"(lo), "=f"(hi)
+          : "r"(h[j]));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[j]) : "f"(hi * d), "f"(lo * d));
+    }
+    *reinterpret_cast<uint4*>(y + row * ldy + col) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
 }
 
 namespace {
@@ -325,7 +415,8 @@ cudaError_t launch_mx4_quant(const Mx4QuantArgs& a, cudaStream_t stream) {
 cudaError_t launch_mx4_dequant(const Mx4DequantArgs& a, cudaStream_t stream) {
   const dim3 block(32, 8);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + 7) / 8), static_cast<unsigned>((a.cols + 255) / 256), 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + 8 * kDequantRows - 1) / (8 * kDequantRows)),
+                     static_cast<unsigned>((a.cols + 255) / 256), 1);
   cfg.blockDim = block;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -25,6 +25,8 @@ COUNTS = {
     "single_rows": [1] * 17,
     "most_empty": [0] * 40 + [5] + [0] * 60 + [260] + [0] * 27,
     "uneven": [513, 2, 64, 0, 255, 384, 7],
+    "few": [12, 0, 16, 33, 5],
+    "some": [40, 0, 65, 20, 1],
 }
 
 
@@ -149,8 +151,14 @@ def _rows_ref(layout, qa, sa, qb, sb, counts, n, k, fmt=0, start=0):
 @pytest.mark.parametrize("layout", [fb.FWD, fb.DGRAD])
 @pytest.mark.parametrize("n,k", [(256, 384), (640, 128)])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
-def test_row_products(counts, layout, n, k, out_dtype):
+@pytest.mark.parametrize("block_n", ["auto", "128", "256"])
+def test_row_products(counts, layout, n, k, out_dtype, block_n, monkeypatch):
+    """Every number of rows through the kernel that the library takes and through the wide-tile ones."""
     require_cuda()
+    if block_n == "256" and n % 256:
+        pytest.skip("N not a multiple of 256")
+    if block_n != "auto":
+        monkeypatch.setenv("FP8BLK_GEMM_BLOCK_N", block_n)
     counts = COUNTS[counts]
     rows = sum(counts)
     rng = np.random.default_rng(rows + n)
@@ -166,11 +174,25 @@ def test_row_products(counts, layout, n, k, out_dtype):
     assert_gemm_close(f32(d), _rows_ref(layout, qa, sa, qb, sb, counts, n, k), f"{counts} layout {layout}")
 
 
-@pytest.mark.parametrize("block_n", ["128", "256"])
-def test_rows_outside_every_group_and_the_row_pitch_stay(block_n, monkeypatch):
+@pytest.mark.parametrize("counts", ["edges", "few", "some", "single_rows"])
+def test_input_gradient_of_e5m2_rows(counts):
+    require_cuda()
+    counts, n, k = COUNTS[counts], 256, 384
+    dy = workloads.grad_output(np.random.default_rng(3), sum(counts), k)
+    qa, sa = _rowwise_ref(dy, True)
+    _, (qb, sb) = _weights(len(counts), k, n, 3)
+    d = fb.fp8blk_gemm_grouped(fb.DGRAD, _f8(qa, True), _dev(sa), _f8(qb), _dev(sb), _offsets(counts))
+    assert fb.fp8blk_get_device_error() == 0
+    assert_gemm_close(f32(d), _rows_ref(fb.DGRAD, qa, sa, qb, sb, counts, n, k, oracle.E5M2), str(counts))
+
+
+@pytest.mark.parametrize("block_n,counts", [("128", [70, 0, 129, 3]), ("256", [70, 0, 129, 3]), ("0", [3, 0, 7, 1, 2]),
+                                            ("0", [3, 0, 40, 1, 2]), ("0", [3, 0, 70, 100, 2])])
+def test_rows_outside_every_group_and_the_row_pitch_stay(block_n, counts, monkeypatch):
     require_cuda()
     monkeypatch.setenv("FP8BLK_GEMM_BLOCK_N", block_n)
-    counts, start, rows, n, k = [70, 0, 129, 3], 6, 260, 256, 256
+    start, n, k = 6, 256, 256
+    rows = start + sum(counts) + 5
     x = workloads.activation(np.random.default_rng(8), rows, k)
     qa, sa = _rowwise_ref(x, False)
     (qb, sb), _ = _weights(len(counts), n, k, 4)
@@ -297,13 +319,13 @@ def test_offsets_that_break_the_rules_write_nothing_out_of_range():
     assert bool((qT[k] == 0x55).all()) and bool((sT[-1] == -7.0).all())
 
 
-@pytest.mark.parametrize("layout", [fb.FWD, fb.WGRAD])
-def test_stalled_grouped_gemm_reports_timeout_and_recovers(layout, monkeypatch):
+@pytest.mark.parametrize("layout,counts", [(fb.FWD, [200, 56]), (fb.FWD, [20, 6]), (fb.WGRAD, [200, 56])])
+def test_stalled_grouped_gemm_reports_timeout_and_recovers(layout, counts, monkeypatch):
     """As tests/test_gpu_timeout.py: a wait that nothing completes ends by its limit."""
     require_cuda()
-    counts, n, k = [200, 56], 256, 256
+    n, k = 256, 256
     rng = np.random.default_rng(3)
-    x, dy = workloads.activation(rng, 256, k), workloads.grad_output(rng, 256, n)
+    x, dy = workloads.activation(rng, sum(counts), k), workloads.grad_output(rng, sum(counts), n)
     off = _offsets(counts)
     (qw, sw), _ = _weights(2, n, k, 5)
     if layout == fb.FWD:

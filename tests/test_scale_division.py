@@ -56,3 +56,18 @@ def test_e5m2_scale_formula_is_correctly_rounded_for_every_bf16_amax():
         if fast_scale(amax, 8192) != want:
             bad.append(bits)
     assert not bad, f"{len(bad)} mismatches, first {[hex(b) for b in bad[:5]]}"
+
+
+def test_sixth_is_correctly_rounded_for_every_bf16_amax():
+    """The 4-bit quantiser's amax / 6 by the same correction: q0 = fl32(a c), fma(fma(-6, q0, a), c, q0)."""
+    c6 = rn32(Fraction(1, 6))
+    assert float(c6).hex() == "0x1.5555560000000p-3"
+    bad = []
+    for bits in range(0, 0x7F80):
+        a = bf16_value(bits)
+        q0 = rn32(a * c6)
+        if rn32(rn32(a - 6 * q0) * c6 + q0) != rn32(a / 6):
+            bad.append(bits)
+    # Below 2^-100 the residual can fall under binary32's range; such a block's
+    # scale rounds to zero with any tensor scale the library documents.
+    assert all(bf16_value(b) < Fraction(2) ** -100 for b in bad), f"{len(bad)} mismatches, first {[hex(b) for b in bad[:5]]}"
