@@ -98,9 +98,18 @@ def _run(device, fn, *args) -> None:
             check(fn(*args))
 
 
+def _empty(shape, dtype, device):
+    """torch.empty for a contiguous tensor, by the entry point that costs the host least."""
+    strides, step = [], 1
+    for size in reversed(shape):
+        strides.append(step)
+        step *= size
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
+
+
 def _out(t, shape, dtype, device):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device)
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"output must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t
@@ -453,7 +462,7 @@ def fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, d=None, stream=None, out_
     if d is None:
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-        d = torch.empty(shape, dtype=out_dtype, device=dev)
+        d = _empty(shape, out_dtype, dev)
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != shape or d.stride(-1) != 1 or (
             layout == WGRAD and groups > 1 and d.stride(0) != m * d.stride(1)):
         raise ValueError(f"d must be a bfloat16 or float32 {shape} tensor with unit column stride and one row pitch")
@@ -464,11 +473,44 @@ def fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, d=None, stream=None, out_
     return d
 
 
+def _keep_for(stream, *tensors) -> None:
+    """Tensors made here and used on a `stream` that was passed in: their memory is not given out again
+    before the work on it is done (without a stream they belong to the current one, as the work does)."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=tensors[0].device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def grouped_linear_forward(x, qw, sw, offsets, stream=None):
     """Y[t] = X[t] . W[e]^T for the rows t of group e: X quantised here (1x128), W [groups,out,in] ahead, as
     one weight of groups*out rows (fp8blk_quantize_weight_128x128: qw [groups*out,in], sw)."""
-    qx, sx, _, _ = fp8blk_quantize_act_1x128_grouped(x, offsets, ROWWISE, stream=stream)
-    return fp8blk_gemm_grouped(FWD, qx, sx, qw, sw, offsets, stream=stream)
+    # The two calls of fp8blk_quantize_act_1x128_grouped and fp8blk_gemm_grouped with one allocation for the
+    # codes and scales between them: with few rows the host's time is what counts.
+    x = _bf16_2d(x)
+    groups = _offsets(offsets)
+    dev = _need_cuda(x, qw, sw, offsets)
+    rows, k = x.shape
+    n = qw.shape[0] // groups
+    if qw.dtype != E4M3 or sw.dtype != torch.float32:
+        raise ValueError("the weight's codes are float8_e4m3fn and its scales float32")
+    if tuple(qw.shape) != (groups * n, k) or tuple(sw.shape) != (groups * n // 128, k // 128):
+        raise ValueError(f"weight {tuple(qw.shape)}, {tuple(sw.shape)} does not match X {tuple(x.shape)} and {groups} groups")
+    if not (qw.is_contiguous() and sw.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous")
+    scales_at = -(-rows * k // 16) * 16
+    work = _empty((scales_at + rows * (k // 128) * 4,), torch.uint8, dev)
+    y = _empty((rows, n), torch.bfloat16, dev)
+    _keep_for(stream, work, y)
+    codes = work.data_ptr()
+    scales, off, handle = codes + scales_at, offsets.data_ptr(), _stream_handle(stream, dev)
+    _run(dev, lib.fp8blk_quantize_act_1x128_grouped, x.data_ptr(), rows, k, max(x.stride(0), k), ROWWISE, off, groups,
+         codes, scales, None, None, handle)
+    _run(dev, lib.fp8blk_gemm_grouped, FWD, groups, off, rows, n, k, codes, scales, qw.data_ptr(), sw.data_ptr(),
+         y.data_ptr(), n, handle)
+    return y
 
 
 def grouped_linear_backward(x, dy, qwT, swT, offsets, stream=None, out_dtype=torch.bfloat16):
@@ -478,6 +520,7 @@ def grouped_linear_backward(x, dy, qwT, swT, offsets, stream=None, out_dtype=tor
     _, _, qxT, sxT = fp8blk_quantize_act_1x128_grouped(x, offsets, COLWISE_T, stream=stream)
     dx = fp8blk_gemm_grouped(DGRAD, qdy, sdy, qwT, swT, offsets, stream=stream)
     dw = fp8blk_gemm_grouped(WGRAD, qdyT, sdyT, qxT, sxT, offsets, stream=stream, out_dtype=out_dtype)
+    _keep_for(stream, qdy, sdy, qdyT, sdyT, qxT, sxT, dx, dw)
     return dx, dw
 
 
@@ -544,7 +587,7 @@ def fp8blk_dequantize_mx4(q, s, fmt, tensor_scale=None, y=None, stream=None):
     dev = _need_cuda(q, s, _tensor_scale(tensor_scale), y)
     rows, cols = _mx4_operand(q, s, fmt, "q")
     if y is None:
-        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        y = _empty((rows, cols), torch.bfloat16, dev)
     elif y.dtype != torch.bfloat16 or tuple(y.shape) != (rows, cols) or y.stride(1) != 1:
         raise ValueError(f"y must be a bfloat16 tensor of shape {(rows, cols)} with unit column stride")
     _run(dev, lib.fp8blk_dequantize_mx4, _ptr(q), _ptr(s), rows, cols, int(fmt), _ptr(tensor_scale), _ptr(y),
@@ -566,7 +609,7 @@ def fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa=None, tensor_sb=None, d=None, s
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
         pitch = -(-n // 8) * 8
-        d = torch.empty((m, pitch), dtype=out_dtype, device=dev)
+        d = _empty((m, pitch), out_dtype, dev)
         if pitch != n:
             d = d[:, :n]
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (m, n) or d.stride(1) != 1:
@@ -579,15 +622,37 @@ def fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa=None, tensor_sb=None, d=None, s
 
 def mx4_linear_forward(x, qw, sw, fmt, x_scale=None, w_scale=None, stream=None):
     """Y = X . W^T in 4 bits: X quantised here, W [out,in] ahead (fp8blk_quantize_mx4, ROWWISE)."""
-    qx, sx, _, _ = fp8blk_quantize_mx4(x, fmt, ROWWISE, x_scale, stream=stream)
-    return fp8blk_gemm_mx4(qx, sx, qw, sw, fmt, x_scale, w_scale, stream=stream)
+    # The two calls of fp8blk_quantize_mx4 and fp8blk_gemm_mx4 with one allocation for the codes and scales
+    # between them: with few rows the host's time is what counts.
+    x = _bf16_2d(x)
+    if fmt not in MX4_BLOCK:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    dev = _need_cuda(x, qw, sw, _tensor_scale(x_scale), _tensor_scale(w_scale))
+    n, k = _mx4_operand(qw, sw, fmt, "W")
+    m = x.shape[0]
+    if x.shape[1] != k:
+        raise ValueError("X and W disagree on their features")
+    scales_at = -(-m * k // 32) * 16
+    blocks, atoms, size = _mx4_scale_shape(fmt, m, k)
+    work = _empty((scales_at + blocks * atoms * size,), torch.uint8, dev)
+    pitch = -(-n // 8) * 8
+    y = _empty((m, pitch), torch.bfloat16, dev)
+    _keep_for(stream, work, y)
+    codes, gx, handle = work.data_ptr(), _ptr(x_scale), _stream_handle(stream, dev)
+    _run(dev, lib.fp8blk_quantize_mx4, x.data_ptr(), m, k, max(x.stride(0), k) if m == 1 else x.stride(0), ROWWISE, fmt,
+         gx, codes, codes + scales_at, None, None, handle)
+    _run(dev, lib.fp8blk_gemm_mx4, fmt, m, n, k, codes, codes + scales_at, gx, qw.data_ptr(), sw.data_ptr(),
+         _ptr(w_scale), y.data_ptr(), pitch, handle)
+    return y if pitch == n else y[:, :n]
 
 
 def mx4_linear_wgrad(x, dy, fmt, x_scale=None, dy_scale=None, stream=None, out_dtype=torch.bfloat16):
     """dW = dY^T . X in 4 bits, both quantised here along the tokens."""
     _, _, qd, sd = fp8blk_quantize_mx4(dy, fmt, COLWISE_T, dy_scale, stream=stream)
     _, _, qx, sx = fp8blk_quantize_mx4(x, fmt, COLWISE_T, x_scale, stream=stream)
-    return fp8blk_gemm_mx4(qd, sd, qx, sx, fmt, dy_scale, x_scale, stream=stream, out_dtype=out_dtype)
+    dw = fp8blk_gemm_mx4(qd, sd, qx, sx, fmt, dy_scale, x_scale, stream=stream, out_dtype=out_dtype)
+    _keep_for(stream, qd, sd, qx, sx, dw)
+    return dw
 
 
 def mx4_linear_backward(x, dy, qwT, swT, fmt, x_scale=None, dy_scale=None, w_scale=None, stream=None,
@@ -598,4 +663,5 @@ def mx4_linear_backward(x, dy, qwT, swT, fmt, x_scale=None, dy_scale=None, w_sca
     _, _, qxT, sxT = fp8blk_quantize_mx4(x, fmt, COLWISE_T, x_scale, stream=stream)
     dx = fp8blk_gemm_mx4(qd, sd, qwT, swT, fmt, dy_scale, w_scale, stream=stream)
     dw = fp8blk_gemm_mx4(qdT, sdT, qxT, sxT, fmt, dy_scale, x_scale, stream=stream, out_dtype=out_dtype)
+    _keep_for(stream, qd, sd, qdT, sdT, qxT, sxT, dx, dw)
     return dx, dw

@@ -118,9 +118,29 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// Register split of the warpgroups (as kLowRegs and kHighRegs): the promotion of
+// 256-column tiles needs a few registers more than gemm.cu's, and its K loop
+// spills with 208 (65536 x 8960 x 1536 over 8 groups: 1054 us; with 216, 1004 us).
+// The other variants do not spill with gemm.cu's split, and would with this one.
+template <int BN, bool kWgrad>
+struct RegSplit {
+  static constexpr int kLow = BN == 256 && !kWgrad ? 72 : kLowRegs;
+  static constexpr int kHigh = BN == 256 && !kWgrad ? 216 : kHighRegs;
+  static_assert(128 * kLow + 256 * kHigh <= kThreads * 168, "register split exceeds the launch allocation");
+};
+
+// Where the promotion warps store a tile, published by the scale producer with
+// the tile's first scales (they have no registers left to find it).  The scale producer is at most kSRing
+// K-blocks, so at most kSRing tiles, ahead of the slowest promotion warp.
+struct TilePlace {
+  int row, col, valid;
+};
+constexpr int kPlaces = 16;
+static_assert(kPlaces > kSRing + 1, "a place is rewritten only after every promotion warp has left its tile");
+
 template <int BN>
 constexpr int grouped_smem_bytes() {
-  return smem_bytes<BN, false>() + kMaxGroups * 4;
+  return smem_bytes<BN, false>() + kPlaces * static_cast<int>(sizeof(TilePlace)) + kMaxGroups * 4;
 }
 static_assert(grouped_smem_bytes<256>() <= 227 * 1024 && grouped_smem_bytes<128>() <= 227 * 1024,
               "shared memory per CTA");
@@ -137,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smem_out = smem + C::kStages * C::kStageBytes;
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem_out + C::kOutBytes);
-  int* ends = reinterpret_cast<int*>(ctrl + 1);
+  TilePlace* places = reinterpret_cast<TilePlace*>(ctrl + 1);
+  int* ends = reinterpret_cast<int*>(places + kPlaces);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -177,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = kWgrad ? p.groups * (p.m / BM) * (p.n / BN) : ends[p.groups - 1] * (p.n / BN);
 
   if (warp < kPromoWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RegSplit<BN, kWgrad>::kLow));
     if (warp == 0 || warp == kBWarp) {
       // ---------------------------------------------------------- operand producers (A: warp 0, B: warp 3)
       const bool is_a = warp == 0;
@@ -219,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int e = 0;
       [[maybe_unused]] float sb0 = 0.0f, sb1 = 0.0f;   // FWD/DGRAD: B scales of K-blocks 32 i + lane
-      for (int u = blockIdx.x; ok && u < tiles; u += gridDim.x) {
+      int n = 0;
+      for (int u = blockIdx.x; ok && u < tiles; u += gridDim.x, ++n) {
         const GroupedTile w = grouped_tile<BN, kWgrad>(p, ends, u, e);
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if constexpr (!kWgrad) {
@@ -251,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               ss.sb[0] = v0;
               if constexpr (BN == 256) ss.sb[1] = v1;
+              if (kb == 0) places[n % kPlaces] = TilePlace{w.a_row, w.out_col, w.valid};
               mbar_arrive(full);                         // releases the stores above
             }
           } else if (lane == 0) {
@@ -282,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kblocks = grouped_kblocks<BN, kWgrad>(p, ends, u);
         for (int kb = 0; kb < kblocks; ++kb) {
           const bool got =
-              mbar_wait_bounded<false>(&ctrl->full[st.idx], st.phase, abort, p.timeout_ns, p.err) &&
-              mbar_wait_bounded<false>(&ctrl->tempty[acc.idx], acc.phase ^ 1u, abort, p.timeout_ns, p.err);
+              mbar_wait_hot(&ctrl->full[st.idx], st.phase, abort, 0, p.timeout_ns, p.err) &&
+              mbar_wait_hot(&ctrl->tempty[acc.idx], acc.phase ^ 1u, abort, 0, p.timeout_ns, p.err);
           if (!__all_sync(0xFFFFFFFFu, got)) {
             ok = false;
             break;
@@ -311,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(&ctrl->mma_done, 0, nullptr, p.timeout_ns, p.err);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RegSplit<BN, kWgrad>::kHigh));
     // ------------------------------------------------------------ promotion + epilogue
     const int ew = warp - kPromoWarp0;  // 0 .. 7
     const int wg = ew >> 2;             // which half of the tile's columns
@@ -322,31 +345,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<C::kAccBufs> tbuf;
     Ring<kSRing> sring;
     float2 acc[BN / 4];
-    bool staged = false;   // this warp's staging area holds a tile whose stores may still be reading it
     int e = 0;
     auto release = [&](int b) {
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->tempty[b]);
     };
-    for (int u = blockIdx.x; u < tiles; u += gridDim.x) {
+    // Read from shared memory in every round: no register is free over the K loop.
+    auto num_tiles = [&]() { return kWgrad ? tiles : ends[p.groups - 1] * (p.n / BN); };
+    for (int u = blockIdx.x; u < num_tiles(); u += gridDim.x) {
       if (!promote_tile<BN, kWgrad>(ctrl, p, acc, grouped_kblocks<BN, kWgrad>(p, ends, u), tmem_lanes, row, col0, tbuf,
                                     sring, abort, lane, release))
         break;
-      const GroupedTile w = grouped_tile<BN, kWgrad>(p, ends, u, e);
+      GroupedTile w;
+      if constexpr (kWgrad) {
+        w = grouped_tile<BN, kWgrad>(p, ends, u, e);
+      } else {
+        const TilePlace at = places[(u / gridDim.x) % kPlaces];
+        w.out_row = at.row;
+        w.out_col = at.col;
+        w.valid = at.valid;
+      }
       const int64_t off = (w.out_row + row) * p.ldd + w.out_col + col0;
       if (p.out_f32) {
         if (kWgrad || row < w.valid) store_row_f32<kCols>(static_cast<float*>(p.d) + off, acc);
-      } else if (!C::kStagedOut || (!kWgrad && quarter * 32 + 32 > w.valid)) {
+      } else if constexpr (!C::kStagedOut) {
         if (kWgrad || row < w.valid) store_row_bf16<kCols>(static_cast<uint16_t*>(p.d) + off, acc);
       } else {
         // As in gemm_blockwise_kernel: the warp's 32 rows x kCols columns in the
-        // 128-byte swizzle of the output map, then TMA stores by one lane.
+        // 128-byte swizzle of the output map, then TMA stores by one lane; or, of a
+        // quarter that the group's last row cuts, its rows by the warp.
         uint8_t* stg = smem_out + ew * (32 * kCols * 2);
-        if (staged) {
-          if (lane == 0) bulk_wait_group_read0();
-          __syncwarp();
-        }
+        if (lane == 0) bulk_wait_group_read0();   // the last tile's stores have read the staging area
+        __syncwarp();
 #pragma unroll
         for (int b = 0; b < kCols / 64; ++b) {
 #pragma unroll
@@ -357,15 +388,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                            pack_bf16x2(a[3].x, a[3].y));
           }
         }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
+        if (kWgrad || quarter * 32 + 32 <= w.valid) {
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
 #pragma unroll
-          for (int b = 0; b < kCols / 64; ++b)
-            tma_store_2d(&tm_d, stg + b * 4096, w.out_col + col0 + b * 64, static_cast<int>(w.out_row) + quarter * 32);
-          bulk_commit_group();
+            for (int b = 0; b < kCols / 64; ++b)
+              tma_store_2d(&tm_d, stg + b * 4096, w.out_col + col0 + b * 64, static_cast<int>(w.out_row) + quarter * 32);
+            bulk_commit_group();
+          }
+        } else {
+          __syncwarp();
+          const int chunk = lane & 15, box = chunk >> 3;       // 16 bytes of a row: two rows a step
+          for (int r = lane >> 4; r < w.valid - quarter * 32; r += 2)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + (w.out_row + quarter * 32 + r) * p.ldd + w.out_col +
+                                      col0 + chunk * 8) =
+                *reinterpret_cast<const uint4*>(stg + box * 4096 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
+          __syncwarp();
         }
-        staged = true;
       }
     }
     if constexpr (C::kStagedOut) {
@@ -752,7 +792,11 @@ cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, cudaStream_t stream) {
   // 46.1 us against 49.5 us (128-row tiles), 16 rows 47.6 to 52.7 us (evenly spread to
   // skewed) against 50.1 us.
   if (!wgrad && g.block_n == 0 && g.rows <= 12 * g.groups) return launch_grouped_few(g, stream);
-  if (g.n % 256 != 0 || g.block_n == 128)
+  // 256-column tiles, unless even the most tiles that the rows can make leave SMs
+  // idle (64 groups of 2560 x 1536, 1024 to 24576 rows: within 4% of 128-column
+  // tiles while the weights' read bounds both, 12 to 15% faster from 12288 rows on).
+  const int64_t most = (wgrad ? g.groups * (g.m / BM) : g.rows / BM + (g.groups < g.rows ? g.groups : g.rows)) * (g.n / 256);
+  if (g.n % 256 != 0 || g.block_n == 128 || (g.block_n == 0 && most < num_sms()))
     return wgrad ? launch_grouped<128, true>(g, stream) : launch_grouped<128, false>(g, stream);
   return wgrad ? launch_grouped<256, true>(g, stream) : launch_grouped<256, false>(g, stream);
 }

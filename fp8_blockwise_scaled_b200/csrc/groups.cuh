@@ -23,6 +23,15 @@ __device__ __forceinline__ int group_rows(const int* offsets, int e, int rows, i
   return begin;
 }
 
+// One warp: ranges[e] = (first row, number of rows) of every group.
+__device__ __forceinline__ void build_ranges(int2* ranges, const int* offsets, int groups, int rows, int lane) {
+  for (int e = lane; e < groups; e += 32) {
+    int size;
+    const int begin = group_rows(offsets, e, rows, &size);
+    ranges[e] = make_int2(begin, size);
+  }
+}
+
 // One warp: ends[e] = number of `block`-row blocks of groups 0 .. e together
 // (never above rows / block + groups, which offsets in order cannot exceed).
 __device__ __forceinline__ void build_block_ends(int* ends, const int* offsets, int groups, int rows, int lane,

@@ -85,12 +85,12 @@ struct QCtrl {
   alignas(16) float4 rq[8][2][4];        // per half-warp, row pair p: {s_2p, s_2p+1, -1/s_2p, -1/s_2p+1}
   alignas(16) uint32_t cpart[8 * 64];    // per-warp packed column maxima (16-byte stores)
 };
-static_assert(sizeof(QCtrl) % 16 == 0, "QCtrl keeps 16-byte alignment");
+static_assert(sizeof(QCtrl) % 16 == 0 && kMaxGroups % 2 == 0, "QCtrl keeps 16-byte alignment");
 constexpr int kCsBytes = kTile * kTile;           // transposed codes, 128-byte rows, 16-B chunks swizzled
 
 template <int MODE, bool kRagged = false>
 __host__ __device__ constexpr int smem_bytes_for() {
-  return (kRagged ? kMaxGroups * 4 : 0) + stages_for<MODE>() * static_cast<int>(kTileBytes) + ((MODE & (Q_COLT | Q_BLKT)) ? kCsBytes : 0) +
+  return (kRagged && (MODE & Q_COLT) ? kMaxGroups * 12 : 0) + stages_for<MODE>() * static_cast<int>(kTileBytes) + ((MODE & (Q_COLT | Q_BLKT)) ? kCsBytes : 0) +
          static_cast<int>(sizeof(QCtrl)) + 1024;  // + alignment slack for the 1024-byte aligned base
 }
 
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
   uint8_t* cs = smem + S * kTileBytes;                                      // [128][128 B] (transposed paths)
   QCtrl* ctrl = reinterpret_cast<QCtrl*>(cs + (kTileSmem ? kCsBytes : 0));
   [[maybe_unused]] int* block_ends = reinterpret_cast<int*>(ctrl + 1);       // kRagged: blocks of groups 0 .. e
+  [[maybe_unused]] int2* ranges = reinterpret_cast<int2*>(block_ends + kMaxGroups);   // and their rows
 
   const int t = threadIdx.x;
   const int lane = t & 31, warp = t >> 5;
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
     const int rows = static_cast<int>(a0.rows);
     if constexpr (kColT) {
       if (warp == 0) build_block_ends(block_ends, a0.offsets, a0.groups, rows, lane);
+      if (warp == 1) build_ranges(ranges, a0.offsets, a0.groups, rows, lane);
       __syncthreads();
       tiles_r = min(static_cast<uint32_t>(block_ends[a0.groups - 1]),
                     static_cast<uint32_t>(a0.padded_rows / kTile));
@@ -192,10 +194,10 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
         lg = static_cast<uint32_t>(find_group(block_ends, a0.groups, static_cast<int>(tr),
                                               tr >= lblock ? static_cast<int>(lg) : 0));
         lblock = tr;
-        int size;
         const int local = static_cast<int>(tr) - (lg ? block_ends[lg - 1] : 0);
-        row0 = group_rows(a0.offsets, static_cast<int>(lg), static_cast<int>(a0.rows), &size) + local * kTile;
-        valid = min(size - local * kTile, kTile);
+        const int2 rows_of = ranges[lg];
+        row0 = rows_of.x + local * kTile;
+        valid = min(rows_of.y - local * kTile, kTile);
       } else {
         row0 = first_row + static_cast<int>(tr) * kTile;
         valid = min(end_row - row0, kTile);

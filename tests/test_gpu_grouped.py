@@ -350,3 +350,44 @@ def test_stalled_grouped_gemm_reports_timeout_and_recovers(layout, counts, monke
         ref = _wgrad_ref(dy, x, counts, False)
         for e in range(2):
             assert_gemm_close(f32(d[e]), ref[e], "after timeout")
+
+
+def test_layer_on_a_stream_that_is_passed_in():
+    """A stream other than the current one, as an object and as a handle, with allocations after the call
+    that would take the memory of the codes if it were given out again."""
+    require_cuda()
+    g, n, k, counts = 3, 256, 384, [200, 0, 129]
+    (qw, sw), (qwT, swT) = _weights(g, n, k, 9)
+    rng = np.random.default_rng(4)
+    X = to_dev(workloads.activation(rng, sum(counts), k))
+    DY = to_dev(workloads.grad_output(rng, sum(counts), n))
+    QW, SW, QWT, SWT, off = _f8(qw), _dev(sw), _f8(qwT), _dev(swT), _offsets(counts)
+    want = (fb.grouped_linear_forward(X, QW, SW, off), *fb.grouped_linear_backward(X, DY, QWT, SWT, off))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)                   # the calls below are queued behind it
+        y = fb.grouped_linear_forward(X, QW, SW, off, stream=stream)
+        dx, dw = fb.grouped_linear_backward(X, DY, QWT, SWT, off, stream=stream)
+        junk = [torch.full((1 << 20,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for a, b in zip((y, dx, dw), want):
+            assert torch.equal(a, b)
+        del junk
+    assert fb.fp8blk_get_device_error() == 0
+
+
+def test_forward_refuses_what_does_not_match():
+    require_cuda()
+    x = torch.zeros((5, 256), dtype=torch.bfloat16, device="cuda")
+    off = _offsets([2, 3])
+    q = torch.zeros((256, 256), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s = torch.ones((2, 2), device="cuda")
+    for bad in (lambda: fb.grouped_linear_forward(x[:, :128], q, s, off), lambda: fb.grouped_linear_forward(x, q, s[:1], off),
+                lambda: fb.grouped_linear_forward(x, q.view(torch.float8_e5m2), s, off),
+                lambda: fb.grouped_linear_forward(x, q.t(), s, off), lambda: fb.grouped_linear_forward(x, q, s.t(), off[:2])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(fb.Fp8BlkError):                  # 64 output columns a group: not a multiple of 128
+        fb.grouped_linear_forward(x, q[:128].contiguous(), s[:1].contiguous(), off)

@@ -303,3 +303,24 @@ def test_large_product(m, n, k, fmt, out_dtype):
     assert fb.fp8blk_get_device_error() == 0
     alpha = 1.0 if g is None else np.float64(np.float32(g) * np.float32(g))
     _assert_product(d, a, b, alpha, k, out_dtype == torch.bfloat16, f"{m} {n} {k} {fmt}")
+
+
+@pytest.mark.parametrize("m", [3, 300])
+def test_layer_on_a_stream_that_is_passed_in(m):
+    require_cuda()
+    n, k = 203, 352
+    X, W, DY = to_dev(_x(m, k, 1, False)), to_dev(_x(n, k, 2, False)), to_dev(_x(m, 208, 3, False))[:, :n]
+    qw, sw, _, _ = fb.fp8blk_quantize_mx4(W, fb.MXFP4)
+    want = fb.mx4_linear_forward(X, qw, sw, fb.MXFP4), fb.mx4_linear_wgrad(X, DY, fb.MXFP4)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+        got = fb.mx4_linear_forward(X, qw, sw, fb.MXFP4, stream=stream), fb.mx4_linear_wgrad(X, DY, fb.MXFP4, stream=stream)
+        junk = [torch.full((1 << 20,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        del junk
+    assert fb.fp8blk_get_device_error() == 0
