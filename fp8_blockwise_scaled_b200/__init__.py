@@ -36,6 +36,7 @@ number of rows in a group):
       COLWISE_T -> q_colT[C,P/2], s_colT for [C,P], P = R rounded up to a multiple of 32
   fp8blk_dequantize_mx4(q, s, fmt) -> bf16 values
   fp8blk_gemm_mx4(a[M,K/2], sa, b[N,K/2], sb, fmt) -> d[M,N]
+  fp8blk_linear_mx4(x[M,K], qw[N,K/2], sw, fmt)    -> d[M,N], x quantised on the way
 """
 from __future__ import annotations
 
@@ -55,7 +56,7 @@ __all__ = [
     "fp8blk_gemm", "fp8blk_gemm_splitk", "fp8blk_gemm_splitk_count", "fp8blk_gemm_splitk_workspace_bytes", "fp8blk_round_f32_to_bf16", "fp8blk_get_device_error", "fp8blk_version", "linear_forward",
     "linear_backward", "fp8blk_grouped_padded_rows", "fp8blk_quantize_act_1x128_grouped", "fp8blk_gemm_grouped",
     "grouped_linear_forward", "grouped_linear_backward", "MAX_GROUPS", "fp8blk_mx4_scale_bytes", "fp8blk_quantize_mx4",
-    "fp8blk_dequantize_mx4", "fp8blk_gemm_mx4", "mx4_linear_forward", "mx4_linear_wgrad", "mx4_linear_backward",
+    "fp8blk_dequantize_mx4", "fp8blk_gemm_mx4", "fp8blk_linear_mx4", "fp8blk_linear_mx4_workspace_bytes", "mx4_linear_forward", "mx4_linear_wgrad", "mx4_linear_backward",
     "MXFP4", "NVFP4", "ROWWISE", "COLWISE_T", "BOTH", "E5M2", "FWD", "DGRAD", "WGRAD", "A_E5M2", "B_E5M2",
     "OUT_F32", "MAX_WEIGHTS", "Fp8BlkError",
     "LIB_PATH", "status_string",
@@ -620,30 +621,54 @@ def fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa=None, tensor_sb=None, d=None, s
     return d
 
 
-def mx4_linear_forward(x, qw, sw, fmt, x_scale=None, w_scale=None, stream=None):
-    """Y = X . W^T in 4 bits: X quantised here, W [out,in] ahead (fp8blk_quantize_mx4, ROWWISE)."""
-    # The two calls of fp8blk_quantize_mx4 and fp8blk_gemm_mx4 with one allocation for the codes and scales
-    # between them: with few rows the host's time is what counts.
+def fp8blk_linear_mx4_workspace_bytes(fmt, m: int, k: int) -> int:
+    """Bytes of workspace fp8blk_linear_mx4 needs for x [m, k]."""
+    return int(lib.fp8blk_linear_mx4_workspace_bytes(int(fmt), int(m), int(k)))
+
+
+def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, workspace=None, stream=None,
+                      out_dtype=torch.bfloat16):
+    """Y = X . W^T in 4 bits, x [M,K] bf16 quantised on the way, W [N,K] ahead (qw [N,K/2], sw): the result of
+    fp8blk_quantize_mx4 and fp8blk_gemm_mx4, in one launch when M <= 16.  workspace: a uint8 CUDA tensor of at
+    least fp8blk_linear_mx4_workspace_bytes(fmt, M, K) bytes (allocated here when None)."""
     x = _bf16_2d(x)
     if fmt not in MX4_BLOCK:
         raise ValueError("fmt must be MXFP4 or NVFP4")
-    dev = _need_cuda(x, qw, sw, _tensor_scale(x_scale), _tensor_scale(w_scale))
+    dev = _need_cuda(x, qw, sw, _tensor_scale(tensor_sx), _tensor_scale(tensor_sw), d, workspace)
     n, k = _mx4_operand(qw, sw, fmt, "W")
     m = x.shape[0]
     if x.shape[1] != k:
         raise ValueError("X and W disagree on their features")
-    scales_at = -(-m * k // 32) * 16
-    blocks, atoms, size = _mx4_scale_shape(fmt, m, k)
-    work = _empty((scales_at + blocks * atoms * size,), torch.uint8, dev)
-    pitch = -(-n // 8) * 8
-    y = _empty((m, pitch), torch.bfloat16, dev)
-    _keep_for(stream, work, y)
-    codes, gx, handle = work.data_ptr(), _ptr(x_scale), _stream_handle(stream, dev)
-    _run(dev, lib.fp8blk_quantize_mx4, x.data_ptr(), m, k, max(x.stride(0), k) if m == 1 else x.stride(0), ROWWISE, fmt,
-         gx, codes, codes + scales_at, None, None, handle)
-    _run(dev, lib.fp8blk_gemm_mx4, fmt, m, n, k, codes, codes + scales_at, gx, qw.data_ptr(), sw.data_ptr(),
-         _ptr(w_scale), y.data_ptr(), pitch, handle)
-    return y if pitch == n else y[:, :n]
+    made = []
+    if workspace is None:
+        blocks, atoms, size = _mx4_scale_shape(fmt, m, k)
+        workspace = _empty((-(-m * k // 32) * 16 + blocks * atoms * size,), torch.uint8, dev)
+        made.append(workspace)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    if d is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        pitch = -(-n // 8) * 8
+        d = _empty((m, pitch), out_dtype, dev)
+        if pitch != n:
+            d = d[:, :n]
+        made.append(d)
+    elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (m, n) or d.stride(1) != 1:
+        raise ValueError("d must be a bfloat16 or float32 [M,N] tensor with unit column stride")
+    pitch, ldx = d.stride(0), x.stride(0)
+    if m == 1:                             # a single row's stride says nothing
+        pitch, ldx = max(pitch, -(-n // 8) * 8), max(ldx, k)
+    _keep_for(stream, *made)
+    _run(dev, lib.fp8blk_linear_mx4, fmt | (OUT_F32 if d.dtype == torch.float32 else 0), m, n, k, x.data_ptr(), ldx,
+         _ptr(tensor_sx), qw.data_ptr(), sw.data_ptr(), _ptr(tensor_sw), workspace.data_ptr(), workspace.numel(),
+         d.data_ptr(), pitch, _stream_handle(stream, dev))
+    return d
+
+
+def mx4_linear_forward(x, qw, sw, fmt, x_scale=None, w_scale=None, stream=None):
+    """Y = X . W^T in 4 bits: X quantised here, W [out,in] ahead (fp8blk_quantize_mx4, ROWWISE)."""
+    return fp8blk_linear_mx4(x, qw, sw, fmt, x_scale, w_scale, stream=stream)
 
 
 def mx4_linear_wgrad(x, dy, fmt, x_scale=None, dy_scale=None, stream=None, out_dtype=torch.bfloat16):

@@ -67,6 +67,8 @@ def _load() -> ctypes.CDLL:
         "fp8blk_quantize_mx4": [P, I64, I64, I64, I, I, P, P, P, P, P, P],
         "fp8blk_dequantize_mx4": [P, P, I64, I64, I, P, P, I64, P],
         "fp8blk_gemm_mx4": [I, I64, I64, I64, P, P, P, P, P, P, P, I64, P],
+        "fp8blk_linear_mx4": [I, I64, I64, I64, P, I64, P, P, P, P, P, I64, P, I64, P],
+        "fp8blk_linear_mx4_workspace_bytes": [I, I64, I64],
         "fp8blk_gemm_splitk": [I, I64, I64, I64, P, P, P, P, P, I64, I, P, I64, P],
         "fp8blk_gemm_splitk_workspace_bytes": [I, I64, I64, I64, I],
         "fp8blk_gemm_splitk_count": [I, I64, I64, I64],
@@ -82,6 +84,7 @@ def _load() -> ctypes.CDLL:
                       "fp8blk_amax_ema_workspace_bytes": ctypes.c_int64,
                       "fp8blk_grouped_padded_rows": ctypes.c_int64,
                       "fp8blk_mx4_scale_bytes": ctypes.c_int64,
+                      "fp8blk_linear_mx4_workspace_bytes": ctypes.c_int64,
                       "fp8blk_gemm_splitk_workspace_bytes": ctypes.c_int64}.get(name, ctypes.c_int)
     return so
 

@@ -486,9 +486,13 @@ fp8blk_status fp8blk_dequantize_mx4(const uint8_t* q, const uint8_t* s, int64_t 
   return launch_status(fp8blk::launch_mx4_dequant(a, static_cast<cudaStream_t>(stream)));
 }
 
-fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const uint8_t* a, const uint8_t* sa,
-                              const float* tensor_sa, const uint8_t* b, const uint8_t* sb, const float* tensor_sb,
-                              void* d, int64_t ldd, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// The checks of a 4-bit product but for its operand a, and its arguments.
+fp8blk_status mx4_gemm_args(int format, int64_t M, int64_t N, int64_t K, const float* tensor_sa, const uint8_t* b,
+                            const uint8_t* sb, const float* tensor_sb, void* d, int64_t ldd, fp8blk::Mx4GemmArgs& g) {
   const bool out_f32 = (format & FP8BLK_OUT_F32) != 0;
   format &= ~FP8BLK_OUT_F32;
   fp8blk_status st = check_mx4(format, tensor_sa);
@@ -497,23 +501,14 @@ fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const
   if (M < 0 || N < 1 || K < 0 || K % 32 != 0) return FP8BLK_ERR_SHAPE;
   if (!mx4_dims_ok(M, N) || !mx4_dims_ok(M, K) || !mx4_dims_ok(N, K)) return FP8BLK_ERR_SHAPE;
   if (ldd < N) return FP8BLK_ERR_INVALID_ARG;
-  if (M == 0) return FP8BLK_OK;
-  if (!d || (K > 0 && (!a || !sa || !b || !sb))) return FP8BLK_ERR_INVALID_ARG;
-  if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(d) ||
-      ldd % (out_f32 ? 4 : 8) != 0)
-    return FP8BLK_ERR_ALIGN;
-  if ((st = check_device()) != FP8BLK_OK) return st;
-  if (K == 0) {   // an empty sum (the weight gradient of no tokens)
-    const size_t size = out_f32 ? 4 : 2;
-    return launch_status(cudaMemset2DAsync(d, ldd * size, 0, N * size, M, static_cast<cudaStream_t>(stream)));
-  }
-  fp8blk::Mx4GemmArgs g{};
+  g = fp8blk::Mx4GemmArgs{};
   g.M = M;
+  if (M == 0) return FP8BLK_OK;
+  if (!d || (K > 0 && (!b || !sb))) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(b) || !aligned16(sb) || !aligned16(d) || ldd % (out_f32 ? 4 : 8) != 0) return FP8BLK_ERR_ALIGN;
   g.N = N;
   g.K = K;
   g.nv = format == FP8BLK_NVFP4;
-  g.a = a;
-  g.sa = sa;
   g.b = b;
   g.sb = sb;
   g.tsa = tensor_sa;
@@ -521,6 +516,13 @@ fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const
   g.d = d;
   g.ldd = ldd;
   g.out_f32 = out_f32;
+  return FP8BLK_OK;
+}
+
+// The rest of the arguments: device, waits, tuning variables.
+fp8blk_status mx4_gemm_device(fp8blk::Mx4GemmArgs& g) {
+  const fp8blk_status st = check_device();
+  if (st != FP8BLK_OK) return st;
   g.timeout_ns = wait_timeout_ns();
   g.err = error_word();
   if (!g.err) return FP8BLK_ERR_CUDA;
@@ -528,7 +530,73 @@ fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const
   g.group_m = env_int("FP8BLK_GEMM_GROUP_M", 0);
   g.pdl = pdl_enabled();
   g.max_ctas = env_int("FP8BLK_GEMM_MAX_CTAS", 0);
+  return FP8BLK_OK;
+}
+
+// An empty sum (the weight gradient of no tokens).
+fp8blk_status mx4_zeros(const fp8blk::Mx4GemmArgs& g, void* stream) {
+  const size_t size = g.out_f32 ? 4 : 2;
+  return launch_status(cudaMemset2DAsync(g.d, g.ldd * size, 0, g.N * size, g.M, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const uint8_t* a, const uint8_t* sa,
+                              const float* tensor_sa, const uint8_t* b, const uint8_t* sb, const float* tensor_sb,
+                              void* d, int64_t ldd, void* stream) {
+  fp8blk::Mx4GemmArgs g;
+  fp8blk_status st = mx4_gemm_args(format, M, N, K, tensor_sa, b, sb, tensor_sb, d, ldd, g);
+  if (st != FP8BLK_OK || M == 0) return st;
+  if (K > 0 && (!a || !sa)) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(sa)) return FP8BLK_ERR_ALIGN;
+  if ((st = mx4_gemm_device(g)) != FP8BLK_OK) return st;
+  if (K == 0) return mx4_zeros(g, stream);
+  g.a = a;
+  g.sa = sa;
   return launch_status(fp8blk::launch_gemm_mx4(g, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t fp8blk_linear_mx4_workspace_bytes(int format, int64_t M, int64_t K) {
+  const int64_t scales = fp8blk_mx4_scale_bytes(format, M, K);
+  if (scales < 0 || K % 32 != 0) return -1;
+  return (M * (K / 2) + 15) / 16 * 16 + scales;
+}
+
+fp8blk_status fp8blk_linear_mx4(int format, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
+                                const float* tensor_sx, const uint8_t* w, const uint8_t* sw, const float* tensor_sw,
+                                void* workspace, int64_t workspace_bytes, void* d, int64_t ldd, void* stream) {
+  fp8blk::Mx4GemmArgs g;
+  fp8blk_status st = mx4_gemm_args(format, M, N, K, tensor_sx, w, sw, tensor_sw, d, ldd, g);
+  if (st != FP8BLK_OK || M == 0) return st;
+  if (ldx < K || (K > 0 && (!x || !workspace))) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(x) || ldx % 8 != 0 || !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
+  const int base = format & ~FP8BLK_OUT_F32;
+  if (workspace_bytes < fp8blk_linear_mx4_workspace_bytes(base, M, K)) return FP8BLK_ERR_INVALID_ARG;
+  if ((st = mx4_gemm_device(g)) != FP8BLK_OK) return st;
+  if (K == 0) return mx4_zeros(g, stream);
+  const uint16_t* xv = static_cast<const uint16_t*>(x);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (fp8blk::mx4_quantizes_on_the_way(M, N, g.max_ctas)) return launch_status(fp8blk::launch_linear_mx4(g, xv, ldx, s));
+  uint8_t* q = static_cast<uint8_t*>(workspace);
+  fp8blk::Mx4QuantArgs a{};
+  a.x = xv;
+  a.rows = M;
+  a.cols = K;
+  a.ldx = ldx;
+  a.nv = g.nv;
+  a.tensor_scale = tensor_sx;
+  a.q_row = q;
+  a.s_row = q + (M * (K / 2) + 15) / 16 * 16;
+  a.timeout_ns = g.timeout_ns;
+  a.err = g.err;
+  a.pdl = g.pdl;
+  a.max_ctas = env_int("FP8BLK_QUANT_MAX_CTAS", 0);
+  if ((st = launch_status(fp8blk::launch_mx4_quant(a, s))) != FP8BLK_OK) return st;
+  g.a = a.q_row;
+  g.sa = a.s_row;
+  return launch_status(fp8blk::launch_gemm_mx4(g, s));
 }
 
 int64_t fp8blk_amax_ema_workspace_bytes(int64_t rows) {

@@ -185,6 +185,11 @@ struct Mx4GemmArgs {
 };
 cudaError_t launch_gemm_mx4(const Mx4GemmArgs& g, cudaStream_t stream);
 
+// The product with a quantised on the way from x [M][ldx] bf16 (g.a and g.sa
+// unused): one launch, for the few rows that mx4_quantizes_on_the_way allows.
+bool mx4_quantizes_on_the_way(int64_t M, int64_t N, int max_ctas);
+cudaError_t launch_linear_mx4(const Mx4GemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream);
+
 // y[i] = bf16_round_nearest_even(x[i]) for i < n (x, y 16-byte aligned).
 cudaError_t launch_round_bf16(const float* x, int64_t n, uint16_t* y, int pdl, cudaStream_t stream);
 

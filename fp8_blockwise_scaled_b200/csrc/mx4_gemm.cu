@@ -592,8 +592,20 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
 // leaves the fp32 partial tile in its shared memory; after a cluster barrier
 // each adds its share of the columns over the partials in the order of their
 // ranks (always the same sum) and stores it.  N = 1536, K = 8960, one row: 15.8 us
-// unsplit.
+// unsplit, 6.4 us split.
+//
+// kQuant: a is not codes but up to 16 rows of bf16 x, quantised on the way by the
+// epilogue's warps (which have nothing else to do yet): a thread turns 32 values
+// of a row into the 16 bytes of codes and the scale bytes that TMA would have
+// brought.  Every CTA of a K range does that again, for a few KB from L2; a launch
+// and a round trip of codes through memory are saved.
 namespace {
+
+// x of a product that quantises on the way.
+struct FewInput {
+  const uint16_t* x;
+  int64_t ldx;
+};
 
 template <int BN, bool kNv>
 struct FewCfg {
@@ -626,11 +638,37 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
 
 }  // namespace
 
-template <int BN, bool kNv>
+// The scale of 16 or 32 values, and their codes: w[0 .. 7] bf16 pairs -> two words a
+// block of 16.
+template <bool kNv>
+__device__ __forceinline__ uint32_t quant_block(const uint4* w, int n, float g, float rg, uint32_t* codes) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < n; ++i)
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[i].x & kAbs2, w[i].y & kAbs2), __vmaxu2(w[i].z & kAbs2, w[i].w & kAbs2)));
+  QScale q;
+  const uint32_t byte = block_scale<kNv>(__uint_as_float(max(m << 16, m & 0xFFFF0000u)), g, rg, q);
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    float x[8], v[8];
+    unpack8(w[i], x);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 r = scaled2<kNv>(make_float2(x[j], x[j + 1]), make_float2(q.s, q.s), make_float2(q.nr, q.nr));
+      v[j] = r.x;
+      v[j + 1] = r.y;
+    }
+    codes[i] = cvt8_e2m1(v) ^ (kNv ? 0x88888888u : 0u);
+  }
+  return byte;
+}
+
+template <int BN, bool kNv, bool kQuant>
 __global__ void __launch_bounds__(kMxThreads, 2)
     gemm_mx4_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                         const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
-                        const Mx4Params p, int splits) {
+                        const Mx4Params p, int splits, const FewInput in) {
+  static_assert(!kQuant || BN == 16, "128 threads quantise 16 rows x 256 values, 32 each");
   using C = FewCfg<BN, kNv>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -642,7 +680,7 @@ __global__ void __launch_bounds__(kMxThreads, 2)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->full[s], kQuant ? 5 : 1);   // the producer, and the warps that quantise
       mbar_init(&ctrl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) mbar_init(&ctrl->sfree[b], 1);
@@ -672,11 +710,13 @@ __global__ void __launch_bounds__(kMxThreads, 2)
         if (!mbar_wait_bounded(&ctrl->empty[st.idx], st.phase ^ 1u, abort, p.timeout_ns, p.err)) break;
         uint8_t* stage = smem + st.idx * C::kStageBytes;
         uint64_t* full = &ctrl->full[st.idx];
-        mbar_arrive_expect_tx(full, C::kStageBytes);
+        mbar_arrive_expect_tx(full, kQuant ? C::kABytes + C::kSfBytes : C::kStageBytes);
         tma_load_2d(stage, &tm_b, full, kb * 128, tile * 128);
-        tma_load_2d(stage + C::kABytes, &tm_a, full, kb * 128, 0);
         tma_load_2d(stage + C::kABytes + C::kBBytes, &tm_sb, full, kb * C::kAtoms * 64, tile);
-        tma_load_2d(stage + C::kABytes + C::kBBytes + C::kSfBytes, &tm_sa, full, kb * C::kAtoms * 64, 0);
+        if constexpr (!kQuant) {
+          tma_load_2d(stage + C::kABytes, &tm_a, full, kb * 128, 0);
+          tma_load_2d(stage + C::kABytes + C::kBBytes + C::kSfBytes, &tm_sa, full, kb * C::kAtoms * 64, 0);
+        }
         ++issued;
         st.next();
       }
@@ -730,6 +770,45 @@ __global__ void __launch_bounds__(kMxThreads, 2)
     __syncwarp();
     // The partial tile takes the stages' place: only when every stage has arrived and been read.
     if (!mbar_wait_bounded(&ctrl->mma_done, 0, nullptr, p.timeout_ns, p.err) || !ok) *abort = 1;
+  } else if (kQuant && warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ x to codes, in the stages' layout
+    const int q = threadIdx.x - 32 * kEpiWarp0, row = q >> 3, part = q & 7;   // values 32 part .. of the stage
+    const float g = kNv && p.tsa ? __ldg(p.tsa) : 1.0f, rg = __frcp_rn(g);
+    const uint16_t* xr = in.x + static_cast<int64_t>(row < p.M ? row : 0) * in.ldx + 32 * part;
+    auto load = [&](int kb, uint4 (&w)[4]) {
+      const int64_t k = static_cast<int64_t>(kb) * kStageK;
+      const bool inside = kb < kb1 && row < p.M && k + 32 * part < p.K;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = inside ? __ldg(reinterpret_cast<const uint4*>(xr + k) + i) : make_uint4(0, 0, 0, 0);
+    };
+    Ring<C::kStages> st;
+    uint4 w[4], next[4];
+    load(kb0, w);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      load(kb + 1, next);                // in flight while this stage's values are turned into codes
+      if (!__all_sync(0xFFFFFFFFu,
+                      mbar_wait_bounded(&ctrl->empty[st.idx], st.phase ^ 1u, abort, p.timeout_ns, p.err)))
+        break;
+      uint8_t* codes = smem + st.idx * C::kStageBytes + C::kABytes;
+      uint8_t* scales = codes + C::kBBytes + C::kSfBytes;
+      uint32_t c[4];
+      if constexpr (kNv) {
+        const uint32_t b0 = quant_block<kNv>(w, 2, g, rg, c), b1 = quant_block<kNv>(w + 2, 2, g, rg, c + 2);
+        *reinterpret_cast<uint16_t*>(scales + (part >> 1) * kMx4AtomBytes + row * 16 + 2 * (part & 1)) =
+            static_cast<uint16_t>(b0 | (b1 << 8));
+      } else {
+        scales[(part >> 2) * kMx4AtomBytes + row * 16 + (part & 3)] =
+            static_cast<uint8_t>(quant_block<kNv>(w, 4, g, rg, c));
+      }
+      *reinterpret_cast<uint4*>(codes + row * 128 + ((part ^ (row & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
+      fence_proxy_async_shared();        // the writes above, then the tensor cores' reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->full[st.idx]);
+      st.next();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = next[i];
+    }
   }
   tc_fence_before_sync();
   __syncthreads();                       // the sums are complete (or a role gave up)
@@ -855,21 +934,27 @@ cudaError_t launch_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int BN, bool kNv>
-cudaError_t launch_mx4_few(const Mx4GemmArgs& g, cudaStream_t stream) {
+template <int BN, bool kNv, bool kQuant>
+cudaError_t launch_mx4_few(const Mx4GemmArgs& g, const FewInput& in, cudaStream_t stream) {
   static PerContext<int> smem_set;
   constexpr int kSmem = few_smem_bytes<BN, kNv>();
-  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_few_kernel<BN, kNv>, kSmem); e != cudaSuccess) return e;
+  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_few_kernel<BN, kNv, kQuant>, kSmem); e != cudaSuccess) return e;
   CUtensorMap ta, tb, tsa, tsb;
-  if (!codes_map(&ta, g.a, g.M, g.K, BN) || !codes_map(&tb, g.b, g.N, g.K, 128) ||
-      !scales_map(&tsa, g.sa, g.M, g.K, kNv, 1) || !scales_map(&tsb, g.sb, g.N, g.K, kNv, 1))
+  if (!codes_map(&tb, g.b, g.N, g.K, 128) || !scales_map(&tsb, g.sb, g.N, g.K, kNv, 1)) return cudaErrorInvalidValue;
+  if constexpr (kQuant) {
+    ta = tb;                             // not used
+    tsa = tsb;
+  } else if (!codes_map(&ta, g.a, g.M, g.K, BN) || !scales_map(&tsa, g.sa, g.M, g.K, kNv, 1)) {
     return cudaErrorInvalidValue;
+  }
   const int64_t tiles = (g.N + 127) / 128, kblocks = (g.K + kStageK - 1) / kStageK;
   // As many CTAs as the SMs hold (two each), every one with at least two stages.
   int splits = 1;
   while (splits < 8 && 2 * splits * tiles <= 2 * num_sms() && kblocks >= 4 * splits) splits *= 2;
   // It is not persistent: a cap on the CTAs is kept by the 1-CTA kernel.
-  if (g.max_ctas > 0 && tiles * splits > g.max_ctas) return launch_mx4<128, kNv>(g, stream);
+  if constexpr (!kQuant) {
+    if (g.max_ctas > 0 && tiles * splits > g.max_ctas) return launch_mx4<128, kNv>(g, stream);
+  }
   const Mx4Params p = mx_params(g, 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), 1, 1);
@@ -883,7 +968,7 @@ cudaError_t launch_mx4_few(const Mx4GemmArgs& g, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1 + set_pdl_attr(attr + 1, g.pdl);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_few_kernel<BN, kNv>, ta, tb, tsa, tsb, p, splits);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_few_kernel<BN, kNv, kQuant>, ta, tb, tsa, tsb, p, splits, in);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -919,15 +1004,25 @@ cudaError_t launch_mx4_pair(const Mx4GemmArgs& g, cudaStream_t stream) {
 
 template <bool kNv>
 cudaError_t launch_mx4_fmt(const Mx4GemmArgs& g, cudaStream_t stream) {
-  if (g.M <= 16) return launch_mx4_few<16, kNv>(g, stream);
-  if (g.M <= 32) return launch_mx4_few<32, kNv>(g, stream);
-  if (g.M <= 64) return launch_mx4_few<64, kNv>(g, stream);
+  if (g.M <= 16) return launch_mx4_few<16, kNv, false>(g, {}, stream);
+  if (g.M <= 32) return launch_mx4_few<32, kNv, false>(g, {}, stream);
+  if (g.M <= 64) return launch_mx4_few<64, kNv, false>(g, {}, stream);
   const int64_t pair_tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
   if (pair_tiles >= num_sms() / 2) return launch_mx4_pair<kNv>(g, stream);
   return launch_mx4<128, kNv>(g, stream);
 }
 
 }  // namespace
+
+bool mx4_quantizes_on_the_way(int64_t M, int64_t N, int max_ctas) {
+  // Without a cap on the CTAs (the kernel is not persistent).
+  return M <= 16 && (max_ctas <= 0 || (N + 127) / 128 * 8 <= max_ctas);
+}
+
+cudaError_t launch_linear_mx4(const Mx4GemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream) {
+  const FewInput in{x, ldx};
+  return g.nv ? launch_mx4_few<16, true, true>(g, in, stream) : launch_mx4_few<16, false, true>(g, in, stream);
+}
 
 cudaError_t launch_gemm_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
   return g.nv ? launch_mx4_fmt<true>(g, stream) : launch_mx4_fmt<false>(g, stream);

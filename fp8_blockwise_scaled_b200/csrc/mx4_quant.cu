@@ -50,36 +50,6 @@ struct Mx4Ctrl {
 constexpr int kSmem = 1024 + kStages * static_cast<int>(kTileBytes) + static_cast<int>(sizeof(Mx4Ctrl));
 static_assert(2 * (kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
 
-// Scale byte of a block of maximum amax, and what its values are divided by.  g
-// and rg = RN(1 / g): the tensor's scale.  Both quotients are correctly rounded
-// by Markstein's correction, as x / s in qmath.cuh: q0 = RN(a y) with y the
-// correctly rounded reciprocal, then RN(q0 + RN(a - q0 b) y).
-template <bool kNv>
-__device__ __forceinline__ uint32_t block_scale(float amax, float g, float rg, QScale& q) {
-  if constexpr (kNv) {
-    constexpr float kSixth = 0x1.555556p-3f;              // RN(1 / 6)
-    const float a0 = amax * kSixth, a = fmaf(fmaf(-6.0f, a0, amax), kSixth, a0);
-    const float t0 = a * rg, t = fmaf(fmaf(-g, t0, a), rg, t0);
-    const uint32_t byte = cvt_e4m3(t);
-    q.s = e4m3_value(byte) * g;
-    q.nr = q.s > 0.0f ? -__frcp_rn(q.s) : 0.0f;
-    return byte;
-  } else {
-    const uint32_t byte = max(static_cast<int>(__float_as_uint(amax) >> 23) - 2, 0);
-    q.s = 0.0f;
-    q.nr = __uint_as_float((254u - byte) << 23);      // 1 / scale, exactly
-    return byte;
-  }
-}
-
-// A pair of values by their blocks' scales: -RN(x / d) (NVFP4, whose code signs
-// are flipped afterwards) or x / scale (MXFP4, exact).
-template <bool kNv>
-__device__ __forceinline__ float2 scaled2(float2 x, float2 s, float2 nr) {
-  if constexpr (kNv) return neg_quotient2(x, s, nr);
-  else return __fmul2_rn(x, nr);
-}
-
 }  // namespace
 
 template <bool kNv, bool kRow, bool kColT>

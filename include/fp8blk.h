@@ -398,6 +398,24 @@ fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const
                               void* d, int64_t ldd, void* stream);
 
 /*
+ * D = X . W^T in 4 bits with X quantised on the way: exactly the result of
+ * fp8blk_quantize_mx4 (ROWWISE) on x [M][ldx] bf16 followed by fp8blk_gemm_mx4
+ * with (w, sw).  With M <= 16 it is one launch that leaves the workspace
+ * unused, else those two.
+ *   workspace   device memory of at least
+ *               fp8blk_linear_mx4_workspace_bytes(format, M, K) bytes, 16-byte
+ *               aligned, owned by the caller, overwritten; two calls may share
+ *               it only if they are ordered (one stream, or events).
+ * Other arguments and errors as for those two calls (K a multiple of 32); the
+ * size is -1 for a bad format, a negative size or K no multiple of 32 (format
+ * without FP8BLK_OUT_F32).
+ */
+int64_t fp8blk_linear_mx4_workspace_bytes(int format, int64_t M, int64_t K);
+fp8blk_status fp8blk_linear_mx4(int format, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
+                                const float* tensor_sx, const uint8_t* w, const uint8_t* sw, const float* tensor_sw,
+                                void* workspace, int64_t workspace_bytes, void* d, int64_t ldd, void* stream);
+
+/*
  * Per-tensor delayed scaling ([EXPL] "核心挑战：Scale Factor 管理", FP8Linear):
  * one amax buffer per tensor (the caller initialises it to 1), updated from
  * the tensor's current max |x| by an exponential moving average before the

@@ -324,3 +324,56 @@ def test_layer_on_a_stream_that_is_passed_in(m):
             assert torch.equal(a, b)
         del junk
     assert fb.fp8blk_get_device_error() == 0
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 32), (1, 1536, 8960), (3, 200, 4128), (7, 136, 96), (16, 264, 1504),
+                                   (16, 130, 288), (17, 264, 544), (200, 72, 320)])
+@pytest.mark.parametrize("fmt,gx,gw", [("mxfp4", None, None), ("nvfp4", None, None), ("nvfp4", 0.0071, 0.5)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_quantised_on_the_way_is_the_two_calls(m, n, k, fmt, gx, gw, out_dtype):
+    """Bit for bit the result of the quantiser and the product; rows of x with a pitch."""
+    require_cuda()
+    f = FORMATS[fmt]
+    x = to_dev(_x(max(m, 3), k + 8, m + n))[:m, :k]
+    qw, sw, _, _ = fb.fp8blk_quantize_mx4(to_dev(_x(n, k, 5, False)), f, fb.ROWWISE, _scalar(gw))
+    qx, sx, _, _ = fb.fp8blk_quantize_mx4(x, f, fb.ROWWISE, _scalar(gx))
+    want = fb.fp8blk_gemm_mx4(qx, sx, qw, sw, f, _scalar(gx), _scalar(gw), out_dtype=out_dtype)
+    size = fb.fp8blk_linear_mx4_workspace_bytes(f, m, k)
+    work = torch.full((size + 64,), 0x55, dtype=torch.uint8, device="cuda")
+    wide = torch.full((m + 1, -(-n // 8) * 8 + 8), 7.0, dtype=out_dtype, device="cuda")
+    got = fb.fp8blk_linear_mx4(x, qw, sw, f, _scalar(gx), _scalar(gw), d=wide[:m, :n], workspace=work[:size])
+    assert fb.fp8blk_get_device_error() == 0
+    assert torch.equal(got, want)
+    assert torch.equal(fb.fp8blk_linear_mx4(x, qw, sw, f, _scalar(gx), _scalar(gw), out_dtype=out_dtype), want)
+    assert bool((work[size:] == 0x55).all()) and bool((wide[m:] == 7.0).all()) and bool((wide[:, n:] == 7.0).all())
+
+
+def test_quantised_on_the_way_under_a_cap_on_the_ctas(monkeypatch):
+    """With few CTAs allowed the two launches run instead; the same values but for the order of the sums."""
+    require_cuda()
+    x, w = to_dev(_x(5, 1536, 1, False)), to_dev(_x(640, 1536, 2, False))
+    qw, sw, _, _ = fb.fp8blk_quantize_mx4(w, fb.NVFP4)
+    want = fb.fp8blk_linear_mx4(x, qw, sw, fb.NVFP4, out_dtype=torch.float32)
+    monkeypatch.setenv("FP8BLK_GEMM_MAX_CTAS", "3")
+    got = fb.fp8blk_linear_mx4(x, qw, sw, fb.NVFP4, out_dtype=torch.float32)
+    assert fb.fp8blk_get_device_error() == 0
+    # Sums of 1536 exact products in fp32, in two orders: each within 1536 2^-24 and 24 steps' 2^-21 of the sum of magnitudes.
+    a, b = (fb.fp8blk_dequantize_mx4(*fb.fp8blk_quantize_mx4(t, fb.NVFP4)[:2], fb.NVFP4).double().abs() for t in (x, w))
+    bound = 2 * (24 * 2.0**-21 + 1536 * 2.0**-24) * (a @ b.t())
+    assert bool(((got.double() - want.double()).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_stalled_product_that_quantises_reports_timeout_and_recovers(fmt, monkeypatch):
+    require_cuda()
+    x, w = to_dev(_x(5, 1536, 1, False)), to_dev(_x(200, 1536, 2, False))
+    qw, sw, _, _ = fb.fp8blk_quantize_mx4(w, FORMATS[fmt])
+    want = fb.fp8blk_linear_mx4(x, qw, sw, FORMATS[fmt])
+    assert fb.fp8blk_get_device_error() == 0
+    monkeypatch.setenv("FP8BLK_TEST_INJECT_STALL", "1")
+    monkeypatch.setenv("FP8BLK_WAIT_TIMEOUT_MS", "200")
+    fb.fp8blk_linear_mx4(x, qw, sw, FORMATS[fmt])
+    assert fb.fp8blk_get_device_error() == 6
+    monkeypatch.delenv("FP8BLK_TEST_INJECT_STALL")
+    assert torch.equal(fb.fp8blk_linear_mx4(x, qw, sw, FORMATS[fmt]), want)
+    assert fb.fp8blk_get_device_error() == 0
