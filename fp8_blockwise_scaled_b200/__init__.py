@@ -29,6 +29,7 @@ number of rows in a group):
       FWD  : a[T,in],  b = q[groups*out,in]            -> Y[T,out]
       DGRAD: a[T,out], b = qT[in,groups*out]           -> dX[T,in]
       WGRAD: a[out,P], b[in,P]                         -> dW[groups,out,in]
+  fp8blk_linear_grouped(x[T,in], q, s, offsets) -> Y[T,out], x quantised on the way
 
 4-bit microscaled formats (MXFP4, NVFP4; codes and scales as uint8, two codes to a byte):
   fp8blk_quantize_mx4(x[R,C], fmt, mode)
@@ -55,6 +56,7 @@ __all__ = [
     "fp8blk_quantize_tensor", "fp8blk_gemm_tensor_scaled", "fp8_linear_delayed_forward",
     "fp8blk_gemm", "fp8blk_gemm_splitk", "fp8blk_gemm_splitk_count", "fp8blk_gemm_splitk_workspace_bytes", "fp8blk_round_f32_to_bf16", "fp8blk_get_device_error", "fp8blk_version", "linear_forward",
     "linear_backward", "fp8blk_grouped_padded_rows", "fp8blk_quantize_act_1x128_grouped", "fp8blk_gemm_grouped",
+    "fp8blk_linear_grouped", "fp8blk_linear_grouped_workspace_bytes",
     "grouped_linear_forward", "grouped_linear_backward", "MAX_GROUPS", "fp8blk_mx4_scale_bytes", "fp8blk_quantize_mx4",
     "fp8blk_dequantize_mx4", "fp8blk_gemm_mx4", "fp8blk_linear_mx4", "fp8blk_linear_mx4_workspace_bytes", "mx4_linear_forward", "mx4_linear_wgrad", "mx4_linear_backward",
     "MXFP4", "NVFP4", "ROWWISE", "COLWISE_T", "BOTH", "E5M2", "FWD", "DGRAD", "WGRAD", "A_E5M2", "B_E5M2",
@@ -485,14 +487,19 @@ def _keep_for(stream, *tensors) -> None:
                 t.record_stream(stream)
 
 
-def grouped_linear_forward(x, qw, sw, offsets, stream=None):
-    """Y[t] = X[t] . W[e]^T for the rows t of group e: X quantised here (1x128), W [groups,out,in] ahead, as
-    one weight of groups*out rows (fp8blk_quantize_weight_128x128: qw [groups*out,in], sw)."""
-    # The two calls of fp8blk_quantize_act_1x128_grouped and fp8blk_gemm_grouped with one allocation for the
-    # codes and scales between them: with few rows the host's time is what counts.
+def fp8blk_linear_grouped_workspace_bytes(rows: int, k: int) -> int:
+    """Bytes of workspace fp8blk_linear_grouped needs for x [rows, k]."""
+    return int(lib.fp8blk_linear_grouped_workspace_bytes(int(rows), int(k)))
+
+
+def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=None, out_dtype=torch.bfloat16):
+    """Y[t] = X[t] . W[e]^T for the rows t of group e, x [T,in] bf16 quantised on the way, W [groups,out,in]
+    ahead as one weight of groups*out rows (qw, sw): the result of fp8blk_quantize_act_1x128_grouped and
+    fp8blk_gemm_grouped, in one launch with few rows a group.  workspace: a uint8 CUDA tensor of at least
+    fp8blk_linear_grouped_workspace_bytes(T, in) bytes (allocated here when None)."""
     x = _bf16_2d(x)
     groups = _offsets(offsets)
-    dev = _need_cuda(x, qw, sw, offsets)
+    dev = _need_cuda(x, qw, sw, offsets, d, workspace)
     rows, k = x.shape
     n = qw.shape[0] // groups
     if qw.dtype != E4M3 or sw.dtype != torch.float32:
@@ -501,17 +508,33 @@ def grouped_linear_forward(x, qw, sw, offsets, stream=None):
         raise ValueError(f"weight {tuple(qw.shape)}, {tuple(sw.shape)} does not match X {tuple(x.shape)} and {groups} groups")
     if not (qw.is_contiguous() and sw.is_contiguous()):
         raise ValueError("codes and scales must be contiguous")
-    scales_at = -(-rows * k // 16) * 16
-    work = _empty((scales_at + rows * (k // 128) * 4,), torch.uint8, dev)
-    y = _empty((rows, n), torch.bfloat16, dev)
-    _keep_for(stream, work, y)
-    codes = work.data_ptr()
-    scales, off, handle = codes + scales_at, offsets.data_ptr(), _stream_handle(stream, dev)
-    _run(dev, lib.fp8blk_quantize_act_1x128_grouped, x.data_ptr(), rows, k, max(x.stride(0), k), ROWWISE, off, groups,
-         codes, scales, None, None, handle)
-    _run(dev, lib.fp8blk_gemm_grouped, FWD, groups, off, rows, n, k, codes, scales, qw.data_ptr(), sw.data_ptr(),
-         y.data_ptr(), n, handle)
-    return y
+    made = []
+    if workspace is None:
+        workspace = _empty((rows * k + rows * (k // 128) * 4,), torch.uint8, dev)
+        made.append(workspace)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    if d is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        d = _empty((rows, n), out_dtype, dev)
+        made.append(d)
+    elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (rows, n) or d.stride(1) != 1:
+        raise ValueError(f"d must be a bfloat16 or float32 {(rows, n)} tensor with unit column stride")
+    pitch, ldx = d.stride(0), x.stride(0)
+    if rows == 1:                          # a single row's stride says nothing
+        pitch, ldx = max(pitch, n), max(ldx, k)
+    _keep_for(stream, *made)
+    _run(dev, lib.fp8blk_linear_grouped, OUT_F32 if d.dtype == torch.float32 else 0, groups, offsets.data_ptr(), rows, n,
+         k, x.data_ptr(), ldx, qw.data_ptr(), sw.data_ptr(), workspace.data_ptr(), workspace.numel(), d.data_ptr(), pitch,
+         _stream_handle(stream, dev))
+    return d
+
+
+def grouped_linear_forward(x, qw, sw, offsets, stream=None):
+    """Y[t] = X[t] . W[e]^T for the rows t of group e: X quantised here (1x128), W [groups,out,in] ahead, as
+    one weight of groups*out rows (fp8blk_quantize_weight_128x128: qw [groups*out,in], sw)."""
+    return fp8blk_linear_grouped(x, qw, sw, offsets, stream=stream)
 
 
 def grouped_linear_backward(x, dy, qwT, swT, offsets, stream=None, out_dtype=torch.bfloat16):

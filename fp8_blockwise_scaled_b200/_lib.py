@@ -69,6 +69,8 @@ def _load() -> ctypes.CDLL:
         "fp8blk_gemm_mx4": [I, I64, I64, I64, P, P, P, P, P, P, P, I64, P],
         "fp8blk_linear_mx4": [I, I64, I64, I64, P, I64, P, P, P, P, P, I64, P, I64, P],
         "fp8blk_linear_mx4_workspace_bytes": [I, I64, I64],
+        "fp8blk_linear_grouped": [I, I64, P, I64, I64, I64, P, I64, P, P, P, I64, P, I64, P],
+        "fp8blk_linear_grouped_workspace_bytes": [I64, I64],
         "fp8blk_gemm_splitk": [I, I64, I64, I64, P, P, P, P, P, I64, I, P, I64, P],
         "fp8blk_gemm_splitk_workspace_bytes": [I, I64, I64, I64, I],
         "fp8blk_gemm_splitk_count": [I, I64, I64, I64],
@@ -84,6 +86,7 @@ def _load() -> ctypes.CDLL:
                       "fp8blk_amax_ema_workspace_bytes": ctypes.c_int64,
                       "fp8blk_grouped_padded_rows": ctypes.c_int64,
                       "fp8blk_mx4_scale_bytes": ctypes.c_int64,
+                      "fp8blk_linear_grouped_workspace_bytes": ctypes.c_int64,
                       "fp8blk_linear_mx4_workspace_bytes": ctypes.c_int64,
                       "fp8blk_gemm_splitk_workspace_bytes": ctypes.c_int64}.get(name, ctypes.c_int)
     return so

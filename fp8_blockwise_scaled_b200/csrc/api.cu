@@ -314,12 +314,19 @@ fp8blk_status fp8blk_gemm(int layout, int64_t M, int64_t N, int64_t K, const uin
   return launch_status(fp8blk::launch_gemm(g, static_cast<cudaStream_t>(stream)));
 }
 
-fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
-                                  const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, void* d,
-                                  int64_t ldd, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// The checks of a grouped product but for its operand a, and its arguments.
+// *nothing: there is nothing to write.
+fp8blk_status grouped_gemm_args(int layout, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                                const uint8_t* b, const float* sb, void* d, int64_t ldd, fp8blk::GroupedGemmArgs& g,
+                                bool* nothing) {
   const int formats = layout & (FP8BLK_A_E5M2 | FP8BLK_B_E5M2);
   const bool out_f32 = (layout & FP8BLK_OUT_F32) != 0;
   layout &= ~(FP8BLK_A_E5M2 | FP8BLK_B_E5M2 | FP8BLK_OUT_F32);
+  *nothing = false;
   if (layout != FP8BLK_FWD && layout != FP8BLK_DGRAD && layout != FP8BLK_WGRAD) return FP8BLK_ERR_INVALID_ARG;
   if (!offsets || groups < 1 || groups > FP8BLK_MAX_GROUPS) return FP8BLK_ERR_INVALID_ARG;
   const bool wgrad = layout == FP8BLK_WGRAD;
@@ -333,17 +340,14 @@ fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* off
       blocks * (N / 128) >= kMost - 1024)
     return FP8BLK_ERR_SHAPE;
   if (ldd < N) return FP8BLK_ERR_INVALID_ARG;
-  if (!wgrad && M == 0) return FP8BLK_OK;
-  if (!b || !sb || !d || (rows != 0 && (!a || !sa))) {
-    if (!d || !(wgrad && rows == 0)) return FP8BLK_ERR_INVALID_ARG;   // WGRAD of no rows writes zeros
+  if (!wgrad && M == 0) {
+    *nothing = true;
+    return FP8BLK_OK;
   }
-  if (!aligned16(a) || !aligned16(b) || (reinterpret_cast<uintptr_t>(d) & 31u) || ldd % (out_f32 ? 8 : 16) != 0)
-    return FP8BLK_ERR_ALIGN;
-  // WGRAD's scales and the per-block scales; FWD and DGRAD read sa by single words.
-  if (!aligned16(sa) || !aligned16(sb) || (reinterpret_cast<uintptr_t>(offsets) & 3u)) return FP8BLK_ERR_ALIGN;
-  fp8blk_status st = check_device();
-  if (st != FP8BLK_OK) return st;
-  fp8blk::GroupedGemmArgs g{};
+  if (!d || ((rows > 0) && (!b || !sb))) return FP8BLK_ERR_INVALID_ARG;   // WGRAD of no rows writes zeros
+  if (!aligned16(b) || (reinterpret_cast<uintptr_t>(d) & 31u) || ldd % (out_f32 ? 8 : 16) != 0) return FP8BLK_ERR_ALIGN;
+  if (!aligned16(sb) || (reinterpret_cast<uintptr_t>(offsets) & 3u)) return FP8BLK_ERR_ALIGN;
+  g = fp8blk::GroupedGemmArgs{};
   g.layout = layout;
   g.groups = groups;
   g.offsets = offsets;
@@ -352,24 +356,83 @@ fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* off
   g.m = wgrad ? M : 0;
   g.n = N;
   g.k = wgrad ? 0 : K;
-  g.a = a;
-  g.sa = sa;
   g.b = b;
   g.sb = sb;
   g.d = d;
   g.ldd = ldd;
   g.out_f32 = out_f32;
+  g.a_e5m2 = (formats & FP8BLK_A_E5M2) != 0;
+  g.b_e5m2 = (formats & FP8BLK_B_E5M2) != 0;
+  return FP8BLK_OK;
+}
+
+// The rest of the arguments: device, waits, tuning variables.
+fp8blk_status grouped_gemm_device(fp8blk::GroupedGemmArgs& g) {
+  const fp8blk_status st = check_device();
+  if (st != FP8BLK_OK) return st;
   g.timeout_ns = wait_timeout_ns();
   g.err = error_word();
   if (!g.err) return FP8BLK_ERR_CUDA;
   g.pdl = pdl_enabled();
-  g.a_e5m2 = (formats & FP8BLK_A_E5M2) != 0;
-  g.b_e5m2 = (formats & FP8BLK_B_E5M2) != 0;
   g.max_ctas = env_int("FP8BLK_GEMM_MAX_CTAS", 0);
   g.group_m = env_int("FP8BLK_GEMM_GROUP_M", 0);
   g.block_n = env_int("FP8BLK_GEMM_BLOCK_N", 0);
   g.inject_stall = env_int("FP8BLK_TEST_INJECT_STALL", 0) != 0;
+  return FP8BLK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                                  const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, void* d,
+                                  int64_t ldd, void* stream) {
+  fp8blk::GroupedGemmArgs g;
+  bool nothing;
+  fp8blk_status st = grouped_gemm_args(layout, groups, offsets, M, N, K, b, sb, d, ldd, g, &nothing);
+  if (st != FP8BLK_OK || nothing) return st;
+  if (g.rows > 0 && (!a || !sa)) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(sa)) return FP8BLK_ERR_ALIGN;
+  if ((st = grouped_gemm_device(g)) != FP8BLK_OK) return st;
+  g.a = a;
+  g.sa = sa;
   return launch_status(fp8blk::launch_gemm_grouped(g, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t fp8blk_linear_grouped_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 0 || K < 0 || K % 128 != 0) return -1;
+  return M * K + M * (K / 128) * 4;
+}
+
+fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                                    const void* x, int64_t ldx, const uint8_t* w, const float* sw, void* workspace,
+                                    int64_t workspace_bytes, void* d, int64_t ldd, void* stream) {
+  if (format & ~FP8BLK_OUT_F32) return FP8BLK_ERR_INVALID_ARG;
+  fp8blk::GroupedGemmArgs g;
+  bool nothing;
+  fp8blk_status st = grouped_gemm_args(FP8BLK_FWD | format, groups, offsets, M, N, K, w, sw, d, ldd, g, &nothing);
+  if (st != FP8BLK_OK || nothing) return st;
+  // The quantiser's limits (fp8blk_quantize_act_1x128_grouped).
+  const int64_t padded = fp8blk_grouped_padded_rows(M, groups);
+  if (padded > (int64_t(1) << 25) || (padded / 128 + 1) * (K / 128) >= (int64_t(1) << 31)) return FP8BLK_ERR_SHAPE;
+  if (!x || ldx < K || !workspace) return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned16(x) || ldx % 8 != 0 || !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
+  if (workspace_bytes < fp8blk_linear_grouped_workspace_bytes(M, K)) return FP8BLK_ERR_INVALID_ARG;
+  if ((st = grouped_gemm_device(g)) != FP8BLK_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint16_t* xv = static_cast<const uint16_t*>(x);
+  if (fp8blk::grouped_few_rows(g)) return launch_status(fp8blk::launch_linear_grouped(g, xv, ldx, s));
+  uint8_t* q = static_cast<uint8_t*>(workspace);
+  QuantArgs a{xv, M, K, ldx, q, reinterpret_cast<float*>(q + M * K), nullptr, nullptr, padded / 128, K / 128};
+  if ((st = set_quant_waits(a)) != FP8BLK_OK) return st;
+  a.offsets = offsets;
+  a.groups = static_cast<int>(groups);
+  a.padded_rows = padded;
+  if ((st = launch_status(fp8blk::launch_quant_grouped(fp8blk::Q_ROW, a, s))) != FP8BLK_OK) return st;
+  g.a = q;
+  g.sa = a.s_row;
+  return launch_status(fp8blk::launch_gemm_grouped(g, s));
 }
 
 int fp8blk_gemm_splitk_count(int layout, int64_t M, int64_t N, int64_t K) {

@@ -30,6 +30,7 @@
 #include "gemm_host.h"
 #include "groups.cuh"
 #include "kernels.h"
+#include "qmath.cuh"
 
 namespace fp8blk {
 
@@ -432,9 +433,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of loads in flight per SM and fill the SMs when there are few tiles.  A group
 // with more than 16 rows takes several tiles of the same weight next to each
 // other, which L2 serves.
+//
+// kQuant: A is bf16 x, quantised on the way by four more warps: per K-block 128
+// threads take 16 values each, reduce a row's 128 over eight lanes, and write the
+// codes in the stage's swizzled layout and the scales into the scale ring, where
+// TMA and cp.async would have put them.  Every column block of a tile's rows does
+// that again, for 4 KB a K-block from L2; a launch and a round trip of codes
+// through memory are saved.
 namespace {
 
 constexpr int kFewThreads = 256;
+constexpr int kFewQuantThreads = 384;    // with the warps that quantise
 constexpr int kFewWarps = 4;             // promotion warps
 constexpr int kFewRows = 16;             // rows of A in a tile
 
@@ -471,6 +480,12 @@ struct FewTile {
   int e, row, col, valid;
 };
 
+// x of a product that quantises on the way.
+struct FewInput {
+  const uint16_t* x;
+  int64_t ldx;
+};
+
 __device__ __forceinline__ FewTile few_tile(const GroupedParams& p, const int* ends, int u, int& e) {
   const int num_nb = p.n / 128;
   e = find_group(ends, p.groups, u / num_nb, e);
@@ -487,9 +502,10 @@ __device__ __forceinline__ FewTile few_tile(const GroupedParams& p, const int* e
 
 }  // namespace
 
-__global__ void __launch_bounds__(kFewThreads, 2)
+template <bool kQuant>
+__global__ void __launch_bounds__(kQuant ? kFewQuantThreads : kFewThreads, 2)
     gemm_grouped_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                            const GroupedParams p) {
+                            const GroupedParams p, const FewInput in) {
   using C = FewCfg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -499,7 +515,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->full[s], kQuant ? 5 : 1);   // the producer, and the warps that quantise
       mbar_init(&ctrl->empty[s], 1);
     }
     for (int b = 0; b < C::kAccBufs; ++b) {
@@ -507,7 +523,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       mbar_init(&ctrl->tempty[b], kFewWarps);
     }
     for (int s = 0; s < kSRing; ++s) {
-      mbar_init(&ctrl->sfull[s], 33);    // every lane's copies, and the B scale
+      mbar_init(&ctrl->sfull[s], kQuant ? 5 : 33);   // the warps that quantise (every lane's copies), and the B scale
       mbar_init(&ctrl->sempty[s], kFewWarps);
     }
     mbar_init(&ctrl->mma_done, 1);
@@ -547,9 +563,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             break;
           }
           uint8_t* stage = smem + st.idx * C::kStageBytes;
-          mbar_arrive_expect_tx(&ctrl->full[st.idx], C::kStageBytes);
+          mbar_arrive_expect_tx(&ctrl->full[st.idx], kQuant ? C::kABytes : C::kStageBytes);
           tma_load_2d(stage, &tm_b, &ctrl->full[st.idx], bx + kb * BK, by);
-          tma_load_2d(stage + C::kABytes, &tm_a, &ctrl->full[st.idx], kb * BK, w.row);
+          if constexpr (!kQuant) tma_load_2d(stage + C::kABytes, &tm_a, &ctrl->full[st.idx], kb * BK, w.row);
           ++issued;
           st.next();
         }
@@ -577,9 +593,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
         FewSlot& ss = ctrl->slots[ring.idx];
         uint64_t* full = &ctrl->sfull[ring.idx];
-        const float* src = p.sa + static_cast<int64_t>(kb) * p.rows + w.row;
-        if (lane < kFewRows) cp_async4(&ss.sa[lane], src + (lane < w.valid ? lane : 0), lane < w.valid);
-        cp_async_arrive(full);
+        if constexpr (!kQuant) {
+          const float* src = p.sa + static_cast<int64_t>(kb) * p.rows + w.row;
+          if (lane < kFewRows) cp_async4(&ss.sa[lane], src + (lane < w.valid ? lane : 0), lane < w.valid);
+          cp_async_arrive(full);
+        }
         const float v = __shfl_sync(0xFFFFFFFFu, sb0, kb & 31);
         if (lane == 0) {
           ss.sb = v;
@@ -629,7 +647,55 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (leader) umma_commit(&ctrl->mma_done);
     __syncwarp();
     mbar_wait_bounded(&ctrl->mma_done, 0, nullptr, p.timeout_ns, p.err);
-  } else if (warp >= 4) {
+  } else if (kQuant && warp >= 8) {
+    // ------------------------------------------------------------ x to codes, in the stages' layout
+    const int q = threadIdx.x - 256, row = q >> 3, part = q & 7;      // values 16 part .. of the K-block
+    Ring<C::kStages> st;
+    Ring<kSRing> ring;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < tiles; u += gridDim.x) {
+      const FewTile w = few_tile(p, ends, u, e);
+      const bool inside = row < w.valid;
+      const uint4* src = reinterpret_cast<const uint4*>(in.x + (w.row + static_cast<int64_t>(inside ? row : 0)) * in.ldx +
+                                                        16 * part);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4 v0 = inside ? __ldg(src) : zero, v1 = inside ? __ldg(src + 1) : zero;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        const bool more = inside && kb + 1 < p.kblocks;               // in flight while this block becomes codes
+        const uint4* ahead = src + 16 * (kb + 1);
+        const uint4 n0 = more ? __ldg(ahead) : zero, n1 = more ? __ldg(ahead + 1) : zero;
+        uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(v0.x & kAbs2, v0.y & kAbs2), __vmaxu2(v0.z & kAbs2, v0.w & kAbs2)),
+                              __vmaxu2(__vmaxu2(v1.x & kAbs2, v1.y & kAbs2), __vmaxu2(v1.z & kAbs2, v1.w & kAbs2)));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const QScale s = make_qscale<false>(__uint_as_float(max(m << 16, m & 0xFFFF0000u)));
+        float x[8];
+        unpack8(v0, x);
+        const uint2 c0 = quant8<false>(x, s);
+        unpack8(v1, x);
+        const uint2 c1 = quant8<false>(x, s);
+        const bool got = mbar_wait_bounded(&ctrl->empty[st.idx], st.phase ^ 1u, abort, p.timeout_ns, p.err) &&
+                         mbar_wait_bounded(&ctrl->sempty[ring.idx], ring.phase ^ 1u, abort, p.timeout_ns, p.err);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          ok = false;
+          break;
+        }
+        *reinterpret_cast<uint4*>(smem + st.idx * C::kStageBytes + C::kABytes + row * 128 + ((part ^ (row & 7)) << 4)) =
+            make_uint4(c0.x, c0.y, c1.x, c1.y);
+        if (part == 0) ctrl->slots[ring.idx].sa[row] = s.s;
+        fence_proxy_async_shared();      // the codes above, then the tensor cores' reads
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctrl->full[st.idx]);
+          mbar_arrive(&ctrl->sfull[ring.idx]);
+        }
+        st.next();
+        ring.next();
+        v0 = n0;
+        v1 = n1;
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ promotion + epilogue
     const int quarter = warp & 3;
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -760,12 +826,18 @@ cudaError_t launch_grouped(const GroupedGemmArgs& g, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_grouped_few(const GroupedGemmArgs& g, cudaStream_t stream) {
+template <bool kQuant>
+cudaError_t launch_grouped_few(const GroupedGemmArgs& g, const FewInput& in, cudaStream_t stream) {
   static PerContext<int> smem_set;
-  if (cudaError_t e = set_smem_once(smem_set, gemm_grouped_few_kernel, kFewSmem); e != cudaSuccess) return e;
+  if (cudaError_t e = set_smem_once(smem_set, gemm_grouped_few_kernel<kQuant>, kFewSmem); e != cudaSuccess) return e;
   const int64_t b_rows = g.layout == 0 ? g.groups * g.n : g.n, b_cols = g.layout == 1 ? g.groups * g.k : g.k;
   CUtensorMap ta, tb;
-  if (!make_map(&ta, g.a, g.rows, g.k, kFewRows) || !make_map(&tb, g.b, b_rows, b_cols, 128)) return cudaErrorInvalidValue;
+  if (!make_map(&tb, g.b, b_rows, b_cols, 128)) return cudaErrorInvalidValue;
+  if constexpr (kQuant) {
+    ta = tb;                             // not used
+  } else if (!make_map(&ta, g.a, g.rows, g.k, kFewRows)) {
+    return cudaErrorInvalidValue;
+  }
   GroupedParams p = grouped_params(g, g.k);
   // The operands' roles are exchanged: the rows' format is the MMA's B format.
   p.fmt_bits = (static_cast<uint32_t>(g.b_e5m2 != 0) << 7) | (static_cast<uint32_t>(g.a_e5m2 != 0) << 10);
@@ -774,24 +846,32 @@ cudaError_t launch_grouped_few(const GroupedGemmArgs& g, cudaStream_t stream) {
   if (g.max_ctas > 0 && g.max_ctas < ctas) ctas = g.max_ctas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(most < ctas ? most : ctas), 1, 1);
-  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.blockDim = dim3(kQuant ? kFewQuantThreads : kFewThreads, 1, 1);
   cfg.dynamicSmemBytes = kFewSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   cfg.numAttrs = set_pdl_attr(attr, g.pdl);
   cfg.attrs = attr;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_grouped_few_kernel, ta, tb, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_grouped_few_kernel<kQuant>, ta, tb, p, in);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
+
+bool grouped_few_rows(const GroupedGemmArgs& g) {
+  return g.layout != 2 && g.block_n == 0 && g.rows <= 12 * g.groups;
+}
+
+cudaError_t launch_linear_grouped(const GroupedGemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream) {
+  return launch_grouped_few<true>(g, FewInput{x, ldx}, stream);
+}
 
 cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, cudaStream_t stream) {
   const bool wgrad = g.layout == 2;
   // Up to 12 rows a group on average; measured with 64 groups of 2560 x 1536: 8 rows
   // 46.1 us against 49.5 us (128-row tiles), 16 rows 47.6 to 52.7 us (evenly spread to
   // skewed) against 50.1 us.
-  if (!wgrad && g.block_n == 0 && g.rows <= 12 * g.groups) return launch_grouped_few(g, stream);
+  if (grouped_few_rows(g)) return launch_grouped_few<false>(g, {}, stream);
   // 256-column tiles, unless even the most tiles that the rows can make leave SMs
   // idle (64 groups of 2560 x 1536, 1024 to 24576 rows: within 4% of 128-column
   // tiles while the weights' read bounds both, 12 to 15% faster from 12288 rows on).

@@ -278,6 +278,23 @@ fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* off
                                   int64_t ldd, void* stream);
 
 /*
+ * FWD with X quantised on the way: exactly the result of
+ * fp8blk_quantize_act_1x128_grouped (ROWWISE) on x [M][ldx] bf16 followed by
+ * fp8blk_gemm_grouped(FP8BLK_FWD) with (w, sw).  With few rows a group (up to 12
+ * on average) it is one launch that leaves the workspace unused, else those two.
+ *   format      0, or FP8BLK_OUT_F32.
+ *   workspace   device memory of at least fp8blk_linear_grouped_workspace_bytes(M, K)
+ *               bytes, 16-byte aligned, owned by the caller, overwritten; two calls
+ *               may share it only if they are ordered (one stream, or events).
+ * Other arguments and errors as for those two calls; the size is -1 for a
+ * negative M or K no multiple of 128.
+ */
+int64_t fp8blk_linear_grouped_workspace_bytes(int64_t M, int64_t K);
+fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                                    const void* x, int64_t ldx, const uint8_t* w, const float* sw, void* workspace,
+                                    int64_t workspace_bytes, void* d, int64_t ldd, void* stream);
+
+/*
  * The same GEMM with split-K, for shapes whose output tiles leave SMs idle:
  * with fewer tiles than SMs (the weight gradient of a narrow layer: few
  * tiles, long K) every tile is split; with more, the tiles of the last,

@@ -391,3 +391,42 @@ def test_forward_refuses_what_does_not_match():
             bad()
     with pytest.raises(fb.Fp8BlkError):                  # 64 output columns a group: not a multiple of 128
         fb.grouped_linear_forward(x, q[:128].contiguous(), s[:1].contiguous(), off)
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=str)
+@pytest.mark.parametrize("n,k", [(128, 384), (384, 1536)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_quantised_on_the_way_is_the_two_calls(counts, n, k, out_dtype):
+    """Bit for bit the result of the quantiser and the product; x and d with a row pitch, rows outside every group."""
+    require_cuda()
+    counts, start = COUNTS[counts], 3
+    rows = start + sum(counts) + 2
+    (qw, sw), _ = _weights(len(counts), n, k, 3)
+    QW, SW, off = _f8(qw), _dev(sw), _offsets(counts, start)
+    x = to_dev(workloads.activation_with_outliers(np.random.default_rng(rows), rows, k + 8, frac=0.01))[:, :k]
+    want = torch.full((rows, n), 7.0, dtype=out_dtype, device="cuda")
+    q, s, _, _ = fb.fp8blk_quantize_act_1x128_grouped(x, off)
+    fb.fp8blk_gemm_grouped(fb.FWD, q, s, QW, SW, off, d=want)
+    size = fb.fp8blk_linear_grouped_workspace_bytes(rows, k)
+    work = torch.full((size + 64,), 0x55, dtype=torch.uint8, device="cuda")
+    wide = torch.full((rows, n + 32), 7.0, dtype=out_dtype, device="cuda")
+    got = fb.fp8blk_linear_grouped(x, QW, SW, off, d=wide[:, :n], workspace=work[:size])
+    assert fb.fp8blk_get_device_error() == 0
+    assert torch.equal(got, want)
+    assert bool((work[size:] == 0x55).all()) and bool((wide[:, n:] == 7.0).all())
+
+
+def test_stalled_product_that_quantises_reports_timeout_and_recovers(monkeypatch):
+    require_cuda()
+    counts, n, k = [7, 0, 3], 256, 384
+    (qw, sw), _ = _weights(3, n, k, 3)
+    x, QW, SW, off = to_dev(workloads.activation(np.random.default_rng(1), 10, k)), _f8(qw), _dev(sw), _offsets(counts)
+    want = fb.fp8blk_linear_grouped(x, QW, SW, off)
+    assert fb.fp8blk_get_device_error() == 0
+    monkeypatch.setenv("FP8BLK_TEST_INJECT_STALL", "1")
+    monkeypatch.setenv("FP8BLK_WAIT_TIMEOUT_MS", "200")
+    fb.fp8blk_linear_grouped(x, QW, SW, off)
+    assert fb.fp8blk_get_device_error() == 6
+    monkeypatch.delenv("FP8BLK_TEST_INJECT_STALL")
+    assert torch.equal(fb.fp8blk_linear_grouped(x, QW, SW, off), want)
+    assert fb.fp8blk_get_device_error() == 0

@@ -80,6 +80,31 @@ def test_gemm_argument_errors(args, code):
     assert _lib.lib.fp8blk_gemm_grouped(*args) == code
 
 
+@pytest.mark.parametrize("args,code", [
+    ((1, 2, A, 5, 128, 128, A, 128, A, A, A, 1 << 20, A, 128, S), 1),      # format
+    ((8, 2, A, 5, 128, 128, A, 128, A, A, A, 1 << 20, A, 128, S), 1),
+    ((0, 2, NULL, 5, 128, 128, A, 128, A, A, A, 1 << 20, A, 128, S), 1),
+    ((0, 2, A, 5, 100, 128, A, 128, A, A, A, 1 << 20, A, 128, S), 2),
+    ((0, 2, A, 1 << 25, 128, 128, A, 128, A, A, A, 1 << 40, A, 128, S), 2),
+    ((0, 2, A, 5, 128, 128, NULL, 128, A, A, A, 1 << 20, A, 128, S), 1),
+    ((0, 2, A, 5, 128, 128, A, 64, A, A, A, 1 << 20, A, 128, S), 1),       # ldx < K
+    ((0, 2, A, 5, 128, 128, A, 132, A, A, A, 1 << 20, A, 128, S), 3),
+    ((0, 2, A, 5, 128, 128, MISALIGNED, 128, A, A, A, 1 << 20, A, 128, S), 3),
+    ((0, 2, A, 5, 128, 128, A, 128, A, A, NULL, 1 << 20, A, 128, S), 1),   # no workspace
+    ((0, 2, A, 5, 128, 128, A, 128, A, A, MISALIGNED, 1 << 20, A, 128, S), 3),
+    ((0, 2, A, 5, 128, 128, A, 128, A, A, A, 5 * 132 - 1, A, 128, S), 1),  # too small
+    ((0, 2, A, 5, 128, 128, A, 128, A, A, A, 1 << 20, A, 64, S), 1),       # ldd < N
+    ((0, 2, A, 0, 128, 128, NULL, 128, A, A, NULL, 0, NULL, 128, S), 0),   # nothing to do
+])
+def test_linear_argument_errors(args, code):
+    assert _lib.lib.fp8blk_linear_grouped(*args) == code
+
+
+def test_linear_workspace():
+    f = fb.fp8blk_linear_grouped_workspace_bytes
+    assert f(5, 256) == 5 * 256 + 5 * 2 * 4 and f(0, 128) == 0 and f(-1, 128) == -1 and f(5, 100) == -1
+
+
 def test_calls_without_rows_need_no_gpu():
     assert _lib.lib.fp8blk_quantize_act_1x128_grouped(NULL, 0, 128, 128, 3, A, 2, NULL, NULL, NULL, NULL, S) == 0
     assert _lib.lib.fp8blk_gemm_grouped(0, 2, A, 0, 128, 128, NULL, NULL, A, A, NULL, 128, S) == 0
