@@ -94,7 +94,7 @@ def _need_cuda(*tensors) -> torch.device:
 def _run(device, fn, *args) -> None:
     """Calls a C entry point with `device` current, so that the library's device
     check, its per-device state and the launch all refer to the tensors' GPU."""
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         check(fn(*args))
     else:
         with torch.cuda.device(device):
@@ -103,11 +103,11 @@ def _run(device, fn, *args) -> None:
 
 def _empty(shape, dtype, device):
     """torch.empty for a contiguous tensor, by the entry point that costs the host least."""
-    strides, step = [], 1
-    for size in reversed(shape):
-        strides.append(step)
-        step *= size
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
+    if len(shape) == 2:
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+    if len(shape) == 1:
+        return torch.empty_strided(shape, (1,), dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _out(t, shape, dtype, device):
@@ -495,7 +495,7 @@ def fp8blk_linear_grouped_workspace_bytes(rows: int, k: int) -> int:
 def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=None, out_dtype=torch.bfloat16):
     """Y[t] = X[t] . W[e]^T for the rows t of group e, x [T,in] bf16 quantised on the way, W [groups,out,in]
     ahead as one weight of groups*out rows (qw, sw): the result of fp8blk_quantize_act_1x128_grouped and
-    fp8blk_gemm_grouped, in one launch with few rows a group.  workspace: a uint8 CUDA tensor of at least
+    fp8blk_gemm_grouped, in one launch with up to 16 rows.  workspace: a uint8 CUDA tensor of at least
     fp8blk_linear_grouped_workspace_bytes(T, in) bytes (allocated here when None)."""
     x = _bf16_2d(x)
     groups = _offsets(offsets)

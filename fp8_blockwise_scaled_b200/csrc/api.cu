@@ -422,7 +422,8 @@ fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* o
   if ((st = grouped_gemm_device(g)) != FP8BLK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint16_t* xv = static_cast<const uint16_t*>(x);
-  if (fp8blk::grouped_few_rows(g)) return launch_status(fp8blk::launch_linear_grouped(g, xv, ldx, s));
+  if (fp8blk::grouped_quantizes_on_the_way(g))
+    return launch_status(fp8blk::launch_linear_grouped(g, xv, ldx, s));
   uint8_t* q = static_cast<uint8_t*>(workspace);
   QuantArgs a{xv, M, K, ldx, q, reinterpret_cast<float*>(q + M * K), nullptr, nullptr, padded / 128, K / 128};
   if ((st = set_quant_waits(a)) != FP8BLK_OK) return st;

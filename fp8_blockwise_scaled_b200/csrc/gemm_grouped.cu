@@ -858,9 +858,19 @@ cudaError_t launch_grouped_few(const GroupedGemmArgs& g, const FewInput& in, cud
 
 }  // namespace
 
+namespace {
+
 bool grouped_few_rows(const GroupedGemmArgs& g) {
   return g.layout != 2 && g.block_n == 0 && g.rows <= 12 * g.groups;
 }
+
+}  // namespace
+
+// Up to 16 rows; then the codes cost more than the launch.  64 groups of 2560 x 1536:
+// 8 rows 11.8 us against 12.8 us for the two launches, 16 rows 17.7 against 17.1,
+// 64 rows 44.4 against 41.0 (the fence between the codes and the tensor cores' reads
+// waits for the loads ahead of it, so every K-block waits for L2).
+bool grouped_quantizes_on_the_way(const GroupedGemmArgs& g) { return g.rows <= 16 && grouped_few_rows(g); }
 
 cudaError_t launch_linear_grouped(const GroupedGemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream) {
   return launch_grouped_few<true>(g, FewInput{x, ldx}, stream);

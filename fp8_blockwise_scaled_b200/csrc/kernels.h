@@ -135,8 +135,8 @@ struct GroupedGemmArgs {
 cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, cudaStream_t stream);
 
 // FWD with A quantised on the way from x [T][ldx] bf16 (g.a and g.sa unused): one
-// launch, where grouped_few_rows(g).
-bool grouped_few_rows(const GroupedGemmArgs& g);
+// launch, where grouped_quantizes_on_the_way(g).
+bool grouped_quantizes_on_the_way(const GroupedGemmArgs& g);
 cudaError_t launch_linear_grouped(const GroupedGemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream);
 
 // 4-bit microscaled quantisation (mx4_quant.cu) and products (mx4_gemm.cu).

@@ -280,8 +280,9 @@ fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* off
 /*
  * FWD with X quantised on the way: exactly the result of
  * fp8blk_quantize_act_1x128_grouped (ROWWISE) on x [M][ldx] bf16 followed by
- * fp8blk_gemm_grouped(FP8BLK_FWD) with (w, sw).  With few rows a group (up to 12
- * on average) it is one launch that leaves the workspace unused, else those two.
+ * fp8blk_gemm_grouped(FP8BLK_FWD) with (w, sw).  With M <= 16 (and at most 12 rows
+ * a group on average) it is one launch that leaves the workspace unused, else
+ * those two.
  *   format      0, or FP8BLK_OUT_F32.
  *   workspace   device memory of at least fp8blk_linear_grouped_workspace_bytes(M, K)
  *               bytes, 16-byte aligned, owned by the caller, overwritten; two calls

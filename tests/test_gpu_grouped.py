@@ -25,6 +25,7 @@ COUNTS = {
     "single_rows": [1] * 17,
     "most_empty": [0] * 40 + [5] + [0] * 60 + [260] + [0] * 27,
     "uneven": [513, 2, 64, 0, 255, 384, 7],
+    "tiny": [3, 0, 5, 2],
     "few": [12, 0, 16, 33, 5],
     "some": [40, 0, 65, 20, 1],
 }
