@@ -118,6 +118,11 @@ def _out(t, shape, dtype, device):
     return t
 
 
+def _pitch(t, width: int) -> int:
+    """Row pitch of a 2-D (or the last two dimensions of a) tensor; a single row's stride says nothing."""
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), width)
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -428,7 +433,7 @@ def fp8blk_quantize_act_1x128_grouped(x, offsets, mode=ROWWISE, q_row=None, s_ro
         s_colT = _out(s_colT, (padded // 128, cols), torch.float32, dev)
     else:
         q_colT = s_colT = None
-    _run(dev, lib.fp8blk_quantize_act_1x128_grouped, _ptr(x), rows, cols, max(x.stride(0), cols), int(mode),
+    _run(dev, lib.fp8blk_quantize_act_1x128_grouped, _ptr(x), rows, cols, _pitch(x, cols), int(mode),
          _ptr(offsets), groups, _ptr(q_row), _ptr(s_row), _ptr(q_colT), _ptr(s_colT), _stream_handle(stream, dev))
     return q_row, s_row, q_colT, s_colT
 
@@ -472,7 +477,7 @@ def fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, d=None, stream=None, out_
     flags = (A_E5M2 if a.dtype == E5M2_DTYPE else 0) | (B_E5M2 if b.dtype == E5M2_DTYPE else 0)
     flags |= OUT_F32 if d.dtype == torch.float32 else 0
     _run(dev, lib.fp8blk_gemm_grouped, int(layout) | flags, groups, _ptr(offsets), m, n, k, _ptr(a), _ptr(sa), _ptr(b),
-         _ptr(sb), _ptr(d), max(d.stride(-2), n), _stream_handle(stream, dev))
+         _ptr(sb), _ptr(d), d.stride(-2) if layout == WGRAD else _pitch(d, n), _stream_handle(stream, dev))
     return d
 
 
@@ -521,9 +526,7 @@ def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=Non
         made.append(d)
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (rows, n) or d.stride(1) != 1:
         raise ValueError(f"d must be a bfloat16 or float32 {(rows, n)} tensor with unit column stride")
-    pitch, ldx = d.stride(0), x.stride(0)
-    if rows == 1:                          # a single row's stride says nothing
-        pitch, ldx = max(pitch, n), max(ldx, k)
+    pitch, ldx = _pitch(d, n), _pitch(x, k)
     _keep_for(stream, *made)
     _run(dev, lib.fp8blk_linear_grouped, OUT_F32 if d.dtype == torch.float32 else 0, groups, offsets.data_ptr(), rows, n,
          k, x.data_ptr(), ldx, qw.data_ptr(), sw.data_ptr(), workspace.data_ptr(), workspace.numel(), d.data_ptr(), pitch,
@@ -598,8 +601,8 @@ def fp8blk_quantize_mx4(x, fmt, mode=ROWWISE, tensor_scale=None, q_row=None, s_r
         s_colT = _out(s_colT, _mx4_scale_shape(fmt, cols, padded), torch.uint8, dev)
     else:
         q_colT = s_colT = None
-    _run(dev, lib.fp8blk_quantize_mx4, _ptr(x), rows, cols, max(x.stride(0), cols) if rows == 1 else x.stride(0),
-         int(mode), int(fmt), _ptr(tensor_scale), _ptr(q_row), _ptr(s_row), _ptr(q_colT), _ptr(s_colT),
+    _run(dev, lib.fp8blk_quantize_mx4, _ptr(x), rows, cols, _pitch(x, cols), int(mode),
+         int(fmt), _ptr(tensor_scale), _ptr(q_row), _ptr(s_row), _ptr(q_colT), _ptr(s_colT),
          _stream_handle(stream, dev))
     return q_row, s_row, q_colT, s_colT
 
@@ -615,7 +618,7 @@ def fp8blk_dequantize_mx4(q, s, fmt, tensor_scale=None, y=None, stream=None):
     elif y.dtype != torch.bfloat16 or tuple(y.shape) != (rows, cols) or y.stride(1) != 1:
         raise ValueError(f"y must be a bfloat16 tensor of shape {(rows, cols)} with unit column stride")
     _run(dev, lib.fp8blk_dequantize_mx4, _ptr(q), _ptr(s), rows, cols, int(fmt), _ptr(tensor_scale), _ptr(y),
-         max(y.stride(0), cols), _stream_handle(stream, dev))
+         _pitch(y, cols), _stream_handle(stream, dev))
     return y
 
 
@@ -638,7 +641,7 @@ def fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa=None, tensor_sb=None, d=None, s
             d = d[:, :n]
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (m, n) or d.stride(1) != 1:
         raise ValueError("d must be a bfloat16 or float32 [M,N] tensor with unit column stride")
-    pitch = max(d.stride(0), -(-n // 8) * 8) if m == 1 else d.stride(0)
+    pitch = _pitch(d, -(-n // 8) * 8)
     _run(dev, lib.fp8blk_gemm_mx4, int(fmt) | (OUT_F32 if d.dtype == torch.float32 else 0), m, n, k, _ptr(a), _ptr(sa),
          _ptr(tensor_sa), _ptr(b), _ptr(sb), _ptr(tensor_sb), _ptr(d), pitch, _stream_handle(stream, dev))
     return d
@@ -679,9 +682,7 @@ def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, wo
         made.append(d)
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (m, n) or d.stride(1) != 1:
         raise ValueError("d must be a bfloat16 or float32 [M,N] tensor with unit column stride")
-    pitch, ldx = d.stride(0), x.stride(0)
-    if m == 1:                             # a single row's stride says nothing
-        pitch, ldx = max(pitch, -(-n // 8) * 8), max(ldx, k)
+    pitch, ldx = _pitch(d, -(-n // 8) * 8), _pitch(x, k)
     _keep_for(stream, *made)
     _run(dev, lib.fp8blk_linear_mx4, fmt | (OUT_F32 if d.dtype == torch.float32 else 0), m, n, k, x.data_ptr(), ldx,
          _ptr(tensor_sx), qw.data_ptr(), sw.data_ptr(), _ptr(tensor_sw), workspace.data_ptr(), workspace.numel(),

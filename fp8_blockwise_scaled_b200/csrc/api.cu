@@ -539,7 +539,7 @@ fp8blk_status fp8blk_dequantize_mx4(const uint8_t* q, const uint8_t* s, int64_t 
                                     const float* tensor_scale, void* y, int64_t ldy, void* stream) {
   fp8blk_status st = check_mx4(format, tensor_scale);
   if (st != FP8BLK_OK) return st;
-  if (rows < 0 || cols < 1 || cols % 32 != 0 || !mx4_dims_ok(rows, cols)) return FP8BLK_ERR_SHAPE;
+  if (rows < 0 || cols < 1 || cols % 32 != 0 || cols > 65535 * 256 || !mx4_dims_ok(rows, cols)) return FP8BLK_ERR_SHAPE;
   if (ldy < cols) return FP8BLK_ERR_INVALID_ARG;
   if (rows == 0) return FP8BLK_OK;
   if (!q || !s || !y) return FP8BLK_ERR_INVALID_ARG;

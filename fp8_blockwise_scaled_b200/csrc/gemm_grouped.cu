@@ -12,8 +12,7 @@
 // The kernel has gemm_blockwise_kernel's roles (two operand producers, MMA
 // issuer, scale producer, eight promotion warps, one persistent CTA per SM)
 // and differs in its tiles, which the host cannot know:
-//   - a warp of every CTA builds the groups' 128-row block counts from the
-//     offsets; tile u is looked up in them (a step or a binary search);
+//   - every CTA builds the groups' 128-row block counts from the offsets; tile u is looked up in them (a step or a binary search);
 //   - FWD / DGRAD tiles start at a group's own rows.  The TMA load of A takes
 //     any first row and may bring rows of the next group or, behind the last
 //     row, zeros; those rows are computed and not stored.  The rows' scales are
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   griddep_wait();   // the offsets may come from the previous kernel
-  if (warp == kScaleWarp) build_block_ends(ends, p.offsets, p.groups, p.rows, lane);
+  build_block_ends(ends, nullptr, p.offsets, p.groups, p.rows, threadIdx.x, kThreads);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -536,7 +535,8 @@ __global__ void __launch_bounds__(kQuant ? kFewQuantThreads : kFewThreads, 2)
     tmem_relinquish();
   }
   griddep_wait();
-  if (warp == kScaleWarp) build_block_ends(ends, p.offsets, p.groups, p.rows, lane, kFewRows);
+  build_block_ends(ends, nullptr, p.offsets, p.groups, p.rows, threadIdx.x, kQuant ? kFewQuantThreads : kFewThreads,
+                   kFewRows);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

@@ -23,32 +23,29 @@ __device__ __forceinline__ int group_rows(const int* offsets, int e, int rows, i
   return begin;
 }
 
-// One warp: ranges[e] = (first row, number of rows) of every group.
-__device__ __forceinline__ void build_ranges(int2* ranges, const int* offsets, int groups, int rows, int lane) {
-  for (int e = lane; e < groups; e += 32) {
+// The whole block (`threads` threads, this one `t`): ends[e] = number of
+// `block`-row blocks of groups 0 .. e together (never above rows / block + groups,
+// which offsets in order cannot exceed), and, unless null, ranges[e] = (first row,
+// number of rows).  All offsets are read at once, one warp adds up.  The caller
+// synchronises the block before it reads the result.
+__device__ __forceinline__ void build_block_ends(int* ends, int2* ranges, const int* offsets, int groups, int rows, int t,
+                                                 int threads, int block = kGroupBlock) {
+  for (int e = t; e < groups; e += threads) {
     int size;
     const int begin = group_rows(offsets, e, rows, &size);
-    ranges[e] = make_int2(begin, size);
+    ends[e] = (size + block - 1) / block;
+    if (ranges) ranges[e] = make_int2(begin, size);
   }
-}
-
-// One warp: ends[e] = number of `block`-row blocks of groups 0 .. e together
-// (never above rows / block + groups, which offsets in order cannot exceed).
-__device__ __forceinline__ void build_block_ends(int* ends, const int* offsets, int groups, int rows, int lane,
-                                                 int block = kGroupBlock) {
+  __syncthreads();
+  if (t >= 32) return;
   const int most = rows / block + groups;
   int before = 0;
   for (int base = 0; base < groups; base += 32) {
-    const int e = base + lane;
-    int n = 0;
-    if (e < groups) {
-      int size;
-      group_rows(offsets, e, rows, &size);
-      n = (size + block - 1) / block;
-    }
+    const int e = base + t;
+    int n = e < groups ? ends[e] : 0;
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xFFFFFFFFu, n, o);
-      if (lane >= o) n = min(n + v, most);
+      if (t >= o) n = min(n + v, most);
     }
     n = min(n + before, most);
     if (e < groups) ends[e] = n;
@@ -67,6 +64,18 @@ __device__ __forceinline__ int find_group(const int* ends, int groups, int b, in
     else lo = mid + 1;
   }
   return lo;
+}
+
+// The same by a whole warp, without a first guess: how many groups end at or before b.
+__device__ __forceinline__ int find_group_warp(const int* ends, int groups, int b, int lane) {
+  int e = 0;
+  for (int base = 0; base < groups; base += 32) {
+    const int i = base + lane;
+    const unsigned before = __ballot_sync(0xFFFFFFFFu, i < groups && ends[i] <= b);
+    e += __popc(before);
+    if (before != 0xFFFFFFFFu) break;
+  }
+  return e;
 }
 
 }  // namespace fp8blk

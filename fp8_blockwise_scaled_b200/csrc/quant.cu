@@ -47,7 +47,7 @@
 // rows; the transposed codes and their scales give every group whole 128-token
 // blocks, one after the other, the last one padded with zero codes.  The
 // number of tiles is known on the device only: every CTA builds the groups'
-// block counts from the offsets (one warp, a scan) before its first load.
+// block counts from the offsets before its first load.
 #include <cuda_fp8.h>
 
 #include <cstring>
@@ -161,8 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
     griddep_wait();                              // the offsets may come from the previous kernel
     const int rows = static_cast<int>(a0.rows);
     if constexpr (kColT) {
-      if (warp == 0) build_block_ends(block_ends, a0.offsets, a0.groups, rows, lane);
-      if (warp == 1) build_ranges(ranges, a0.offsets, a0.groups, rows, lane);
+      build_block_ends(block_ends, ranges, a0.offsets, a0.groups, rows, t, kThreads);
       __syncthreads();
       tiles_r = min(static_cast<uint32_t>(block_ends[a0.groups - 1]),
                     static_cast<uint32_t>(a0.padded_rows / kTile));
@@ -183,31 +182,34 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
       ++tc;
     }
   };
+  // kRagged: first row and number of rows of row block tr.  Called by the whole
+  // warp 0: its other lanes help to find the group, since every warp waits for
+  // thread 0 at the next barrier.
+  [[maybe_unused]] int place_row = 0, place_rows = 0;
+  [[maybe_unused]] auto find_place = [&](uint32_t tr) {
+    if constexpr (kColT) {
+      const int e = find_group_warp(block_ends, a0.groups, static_cast<int>(tr), lane);
+      const int local = static_cast<int>(tr) - (e ? block_ends[e - 1] : 0);
+      const int2 rows_of = ranges[e];
+      place_row = rows_of.x + local * kTile;
+      place_rows = min(rows_of.y - local * kTile, kTile);
+    } else {
+      place_row = first_row + static_cast<int>(tr) * kTile;
+      place_rows = min(end_row - place_row, kTile);
+    }
+  };
   // Loads tile j into `stage`; (ltr, ltc) are its coordinates when N == 1.
-  uint32_t lg = 0;                                                   // tensor (N > 1) or group of the last load
-  [[maybe_unused]] uint32_t lblock = 0;                              // kRagged: row block of the last load
+  uint32_t lg = 0;                                                   // tensor of the last load (N > 1)
   auto load_tile = [&](int stage, uint32_t j, uint32_t ltr, uint32_t ltc) {
     uint32_t g = 0, tr = ltr, tc = ltc;
     if constexpr (kRagged) {
-      int row0, valid;
-      if constexpr (kColT) {
-        lg = static_cast<uint32_t>(find_group(block_ends, a0.groups, static_cast<int>(tr),
-                                              tr >= lblock ? static_cast<int>(lg) : 0));
-        lblock = tr;
-        const int local = static_cast<int>(tr) - (lg ? block_ends[lg - 1] : 0);
-        const int2 rows_of = ranges[lg];
-        row0 = rows_of.x + local * kTile;
-        valid = min(rows_of.y - local * kTile, kTile);
-      } else {
-        row0 = first_row + static_cast<int>(tr) * kTile;
-        valid = min(end_row - row0, kTile);
-      }
-      ctrl->coord[stage][0] = static_cast<uint32_t>(row0);
-      ctrl->coord[stage][1] = static_cast<uint32_t>(valid);
+      ctrl->coord[stage][0] = static_cast<uint32_t>(place_row);
+      ctrl->coord[stage][1] = static_cast<uint32_t>(place_rows);
       ctrl->coord[stage][2] = tc;
       ctrl->coord[stage][3] = tr;
       mbar_arrive_expect_tx(&ctrl->full[stage], kTileBytes);   // rows behind the tensor arrive as zeros
-      tma_load_2d(smem + stage * kTileBytes, &L.map[0], &ctrl->full[stage], static_cast<int>(tc * kTile), row0);
+      tma_load_2d(smem + stage * kTileBytes, &L.map[0], &ctrl->full[stage], static_cast<int>(tc * kTile),
+                  place_row);
       return;
     }
     if constexpr (N > 1) {
@@ -238,8 +240,12 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
     fence_mbar_init();
     for (int g = 0; g < N; ++g) tma_prefetch_map(&L.map[g]);
     griddep_wait();                              // the input may come from the previous kernel
+  }
+  if (kRagged ? warp == 0 : t == 0) {
     for (uint32_t j = blockIdx.x; issued < static_cast<uint32_t>(S) && j < tiles; j += gridDim.x) {
-      load_tile(static_cast<int>(issued++), j, ltr, ltc);
+      if constexpr (kRagged) find_place(ltr);
+      if (t == 0) load_tile(static_cast<int>(issued), j, ltr, ltc);
+      ++issued;
       advance(ltr, ltc);
     }
   }
@@ -306,8 +312,14 @@ __global__ void __launch_bounds__(kThreads, 2) quant_tile_kernel(const __grid_co
     }
     __syncwarp();                                // everything else comes from registers: hand the stage back
     if (lane == 0) mbar_arrive(&ctrl->empty[s]);
+    const uint32_t next = tile + static_cast<uint32_t>(S) * gridDim.x;
+    if constexpr (kRagged) {
+      if (warp == 0 && next < tiles) {
+        find_place(ltr);
+        if (t != 0) advance(ltr, ltc);           // thread 0 does so below
+      }
+    }
     if (t == 0) {                                // and refill it with the tile S steps ahead
-      const uint32_t next = tile + static_cast<uint32_t>(S) * gridDim.x;
       if (next < tiles && mbar_wait_bounded<false>(&ctrl->empty[s], ph, abort, a0.timeout_ns, a0.err)) {
         // The warps read the stage through the generic proxy; the TMA load
         // rewrites it through the async proxy: order the two.

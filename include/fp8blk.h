@@ -391,7 +391,8 @@ fp8blk_status fp8blk_quantize_mx4(const void* x, int64_t rows, int64_t cols, int
 /*
  * The values of 4-bit codes: y[r][c] = bf16(fl32(q * d)), d = the block's scale
  * (fl32(sf * g) for FP8BLK_NVFP4).  q [rows][cols/2] and s as above (also a
- * COLWISE_T pair, with its rows = cols and cols = P); cols a multiple of 32;
+ * COLWISE_T pair, with its rows = cols and cols = P); cols a multiple of 32, at
+ * most 16776960;
  * y [rows][ldy] bf16, 16-byte aligned, ldy a multiple of 8.
  */
 fp8blk_status fp8blk_dequantize_mx4(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, int format,
