@@ -78,6 +78,15 @@ int pdl_enabled() {
   return e ? std::atoi(e) != 0 : 0;
 }
 
+// Rows sorted by group, up to 64 a group on average: dependent launch always.  There
+// the kernels are short enough for their prologues (barriers, tensor memory, the
+// groups' table) to show: 509 rows in 64 groups forward 50.3 -> 45.7 us, 1003 rows in
+// 16 groups backward 78.5 -> 72.1 us; with 1024 rows a group 2% slower, as above.
+// `slack`: padding a group that the rows may hold.
+int grouped_pdl(int64_t rows, int64_t groups, int64_t slack) {
+  return rows <= (64 + slack) * groups ? 1 : pdl_enabled();
+}
+
 int env_int(const char* name, int fallback) {
   const char* e = std::getenv(name);
   return e ? std::atoi(e) : fallback;
@@ -179,6 +188,7 @@ fp8blk_status fp8blk_quantize_act_1x128_grouped(const void* x, int64_t rows, int
   QuantArgs a{static_cast<const uint16_t*>(x), rows, cols, ldx, q_row, s_row, q_colT, s_colT, padded / 128,
               cols / 128};
   if ((st = set_quant_waits(a)) != FP8BLK_OK) return st;
+  a.pdl = grouped_pdl(rows, groups, 0);
   a.offsets = offsets;
   a.groups = static_cast<int>(groups);
   a.padded_rows = padded;
@@ -373,7 +383,7 @@ fp8blk_status grouped_gemm_device(fp8blk::GroupedGemmArgs& g) {
   g.timeout_ns = wait_timeout_ns();
   g.err = error_word();
   if (!g.err) return FP8BLK_ERR_CUDA;
-  g.pdl = pdl_enabled();
+  g.pdl = grouped_pdl(g.rows, g.groups, g.layout == FP8BLK_WGRAD ? 128 : 0);
   g.max_ctas = env_int("FP8BLK_GEMM_MAX_CTAS", 0);
   g.group_m = env_int("FP8BLK_GEMM_GROUP_M", 0);
   g.block_n = env_int("FP8BLK_GEMM_BLOCK_N", 0);
@@ -427,6 +437,7 @@ fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* o
   uint8_t* q = static_cast<uint8_t*>(workspace);
   QuantArgs a{xv, M, K, ldx, q, reinterpret_cast<float*>(q + M * K), nullptr, nullptr, padded / 128, K / 128};
   if ((st = set_quant_waits(a)) != FP8BLK_OK) return st;
+  a.pdl = g.pdl;
   a.offsets = offsets;
   a.groups = static_cast<int>(groups);
   a.padded_rows = padded;
