@@ -118,14 +118,14 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Register split of the warpgroups (as kLowRegs and kHighRegs): the promotion of
-// 256-column tiles needs a few registers more than gemm.cu's, and its K loop
-// spills with 208 (65536 x 8960 x 1536 over 8 groups: 1054 us; with 216, 1004 us).
-// The other variants do not spill with gemm.cu's split, and would with this one.
+// Register split of the warpgroups (as kLowRegs and kHighRegs).  With 256-column
+// tiles of rows the scale producer needs more than 80 registers and the promotion
+// no more than 200: 88 / 200 spills nothing, 80 / 208 does (65536 x 8960 x 1536 over
+// 8 groups: 972 us against 1054 us).
 template <int BN, bool kWgrad>
 struct RegSplit {
-  static constexpr int kLow = BN == 256 && !kWgrad ? 72 : kLowRegs;
-  static constexpr int kHigh = BN == 256 && !kWgrad ? 216 : kHighRegs;
+  static constexpr int kLow = BN == 256 && !kWgrad ? 88 : kLowRegs;
+  static constexpr int kHigh = BN == 256 && !kWgrad ? 200 : kHighRegs;
   static_assert(128 * kLow + 256 * kHigh <= kThreads * 168, "register split exceeds the launch allocation");
 };
 
@@ -351,8 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->tempty[b]);
     };
-    // Read from shared memory in every round: no register is free over the K loop.
-    auto num_tiles = [&]() { return kWgrad ? tiles : ends[p.groups - 1] * (p.n / BN); };
+    // Read from shared memory in every round, so that no register holds it over the K loop.
+    auto num_tiles = [&]() {
+      if constexpr (kWgrad) return tiles;
+      int blocks;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(blocks) : "r"(smem_addr(ends + p.groups - 1)) : "memory");
+      return blocks * (p.n / BN);
+    };
     for (int u = blockIdx.x; u < num_tiles(); u += gridDim.x) {
       if (!promote_tile<BN, kWgrad>(ctrl, p, acc, grouped_kblocks<BN, kWgrad>(p, ends, u), tmem_lanes, row, col0, tbuf,
                                     sring, abort, lane, release))
