@@ -630,9 +630,12 @@ constexpr int few_smem_bytes() {
 static_assert(2 * (few_smem_bytes<64, true>() + 1024) <= 227 * 1024 && 2 * (few_smem_bytes<32, true>() + 1024) <= 227 * 1024,
               "two CTAs per SM");
 
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -837,24 +840,45 @@ __global__ void __launch_bounds__(kMxThreads, 2)
   // Column n of the tile: this CTA's share is 128 / splits of them.
   if (done) {
     const float alpha = (p.tsa ? __ldg(p.tsa) : 1.0f) * (p.tsb ? __ldg(p.tsb) : 1.0f);
-    const int share = 128 / splits;
+    // Four columns a thread and step; the partials of all ranks are loaded before any is added.
+    const int share = 128 / splits, quads = share / 4;
     const uint32_t part0 = smem_addr(part);
-    for (int i = threadIdx.x; i < rows * share; i += kMxThreads) {
-      const int m = i / share, n = rank * share + (i - m * share);
+    for (int i = threadIdx.x; i < rows * quads; i += kMxThreads) {
+      const int m = i / quads, n = rank * share + 4 * (i - m * quads);
       const uint32_t at = part0 + static_cast<uint32_t>(m * 128 + n) * 4;
-      float sum = 0.0f;
-      if (splits > 1) {
-        for (int s = 0; s < splits; ++s) sum += ld_shared_cluster_f32(mapa_shared(at, s));
-      } else {
-        sum = part[m * 128 + n];
+      float4 v[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < splits) v[s] = ld_shared_cluster_v4(mapa_shared(at, s));
+      float4 sum = v[0];
+#pragma unroll
+      for (int s = 1; s < 8; ++s) {
+        if (s < splits) {
+          sum.x += v[s].x;
+          sum.y += v[s].y;
+          sum.z += v[s].z;
+          sum.w += v[s].w;
+        }
       }
+      const float out[4] = {sum.x * alpha, sum.y * alpha, sum.z * alpha, sum.w * alpha};
       const int64_t col = static_cast<int64_t>(tile) * 128 + n;
-      if (col < p.N) {
-        const float v = sum * alpha;
+      float* df = static_cast<float*>(p.d) + m * p.ldd + col;
+      __nv_bfloat16* db = static_cast<__nv_bfloat16*>(p.d) + m * p.ldd + col;
+      if (col + 4 <= p.N) {
         if (p.out_f32)
-          static_cast<float*>(p.d)[m * p.ldd + col] = v;
+          *reinterpret_cast<float4*>(df) = make_float4(out[0], out[1], out[2], out[3]);
         else
-          static_cast<__nv_bfloat16*>(p.d)[m * p.ldd + col] = __float2bfloat16_rn(v);
+          *reinterpret_cast<uint2*>(db) = make_uint2(pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (col + j < p.N) {
+            if (p.out_f32)
+              df[j] = out[j];
+            else
+              db[j] = __float2bfloat16_rn(out[j]);
+          }
+        }
       }
     }
   }
