@@ -697,11 +697,35 @@ def mx4_linear_forward(x, qw, sw, fmt, x_scale=None, w_scale=None, stream=None):
 
 def mx4_linear_wgrad(x, dy, fmt, x_scale=None, dy_scale=None, stream=None, out_dtype=torch.bfloat16):
     """dW = dY^T . X in 4 bits, both quantised here along the tokens."""
-    _, _, qd, sd = fp8blk_quantize_mx4(dy, fmt, COLWISE_T, dy_scale, stream=stream)
-    _, _, qx, sx = fp8blk_quantize_mx4(x, fmt, COLWISE_T, x_scale, stream=stream)
-    dw = fp8blk_gemm_mx4(qd, sd, qx, sx, fmt, dy_scale, x_scale, stream=stream, out_dtype=out_dtype)
-    _keep_for(stream, qd, sd, qx, sx, dw)
-    return dw
+    # The calls of fp8blk_quantize_mx4 (COLWISE_T, twice) and fp8blk_gemm_mx4 with one allocation for the codes
+    # and scales between them: with few tokens the host's time is what counts.
+    x, dy = _bf16_2d(x), _bf16_2d(dy)
+    if fmt not in MX4_BLOCK:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    dev = _need_cuda(x, dy, _tensor_scale(x_scale), _tensor_scale(dy_scale))
+    tokens, k = x.shape
+    n = dy.shape[1]
+    if dy.shape[0] != tokens:
+        raise ValueError("X and dY disagree on their tokens")
+    padded = -(-tokens // 32) * 32
+    at, places = 0, []                     # codes and scales of dY, then of X, all on 16-byte boundaries
+    for rows in (n, k):
+        blocks, atoms, size = _mx4_scale_shape(fmt, rows, padded)
+        places += [at, at + rows * padded // 2]
+        at = places[-1] + blocks * atoms * size
+    work = _empty((at,), torch.uint8, dev)
+    pitch = -(-k // 8) * 8
+    dw = _empty((n, pitch), out_dtype, dev)
+    _keep_for(stream, work, dw)
+    base, handle, gx, gd = work.data_ptr(), _stream_handle(stream, dev), _ptr(x_scale), _ptr(dy_scale)
+    qd, sd, qx, sx = (base + p for p in places) if tokens else (None,) * 4
+    _run(dev, lib.fp8blk_quantize_mx4, dy.data_ptr(), tokens, n, _pitch(dy, n), COLWISE_T, fmt, gd, None, None, qd, sd, handle)
+    _run(dev, lib.fp8blk_quantize_mx4, x.data_ptr(), tokens, k, _pitch(x, k), COLWISE_T, fmt, gx, None, None, qx, sx, handle)
+    _run(dev, lib.fp8blk_gemm_mx4, fmt | (OUT_F32 if out_dtype == torch.float32 else 0), n, k, padded, qd, sd, gd, qx, sx,
+         gx, dw.data_ptr(), pitch, handle)
+    return dw if pitch == k else dw[:, :k]
 
 
 def mx4_linear_backward(x, dy, qwT, swT, fmt, x_scale=None, dy_scale=None, w_scale=None, stream=None,
