@@ -40,14 +40,15 @@ __device__ __forceinline__ uint32_t cvt8_e2m1(const float (&x)[8]) {
   return r;
 }
 
-// Two values -> two codes in the low byte, x0 in the low nibble.
-__device__ __forceinline__ uint32_t cvt2_e2m1(float x0, float x1) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
-      "cvt.u32.u8 %0, t;\n\t}"
-      : "=r"(r)
-      : "f"(x0), "f"(x1));
+// Four values -> four codes, x0 in the lowest nibble.
+__device__ __forceinline__ uint16_t cvt4_e2m1(float x0, float x1, float x2, float x3) {
+  uint16_t r;
+  asm("{\n\t.reg .b8 a, b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "mov.b16 %0, {a, b};\n\t}"
+      : "=h"(r)
+      : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
   return r;
 }
 
@@ -72,18 +73,30 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
 }
 
 // Scale byte of a block of maximum amax, and what its values are divided by.  g
-// and rg = RN(1 / g): the tensor's scale.  Both quotients are correctly rounded
-// by Markstein's correction, as x / s in qmath.cuh: q0 = RN(a y) with y the
-// correctly rounded reciprocal, then RN(q0 + RN(a - q0 b) y).
+// and rg = RN(1 / g): the tensor's scale.  amax / 6 and that by g are correctly
+// rounded by Markstein's correction, as x / s in qmath.cuh: q0 = RN(a y) with y
+// the correctly rounded reciprocal, then RN(q0 + RN(a - q0 b) y).
+// The scale byte of an NVFP4 block of maximum amax.
+__device__ __forceinline__ uint32_t nvfp4_scale(float amax, float g, float rg) {
+  constexpr float kSixth = 0x1.555556p-3f;              // RN(1 / 6)
+  const float a0 = amax * kSixth, a = fmaf(fmaf(-6.0f, a0, amax), kSixth, a0);
+  const float t0 = a * rg, t = fmaf(fmaf(-g, t0, a), rg, t0);
+  return cvt_e4m3(t);
+}
+
+// What the values of an NVFP4 block with that scale byte are divided by.
+__device__ __forceinline__ QScale nvfp4_divisor(uint32_t byte, float g) {
+  QScale q;
+  q.s = e4m3_value(byte) * g;
+  q.nr = q.s > 0.0f ? -__frcp_rn(q.s) : 0.0f;
+  return q;
+}
+
 template <bool kNv>
 __device__ __forceinline__ uint32_t block_scale(float amax, float g, float rg, QScale& q) {
   if constexpr (kNv) {
-    constexpr float kSixth = 0x1.555556p-3f;              // RN(1 / 6)
-    const float a0 = amax * kSixth, a = fmaf(fmaf(-6.0f, a0, amax), kSixth, a0);
-    const float t0 = a * rg, t = fmaf(fmaf(-g, t0, a), rg, t0);
-    const uint32_t byte = cvt_e4m3(t);
-    q.s = e4m3_value(byte) * g;
-    q.nr = q.s > 0.0f ? -__frcp_rn(q.s) : 0.0f;
+    const uint32_t byte = nvfp4_scale(amax, g, rg);
+    q = nvfp4_divisor(byte, g);
     return byte;
   } else {
     const uint32_t byte = max(static_cast<int>(__float_as_uint(amax) >> 23) - 2, 0);

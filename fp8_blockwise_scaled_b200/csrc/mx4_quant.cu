@@ -19,8 +19,11 @@
 // 8 and 16 apart, so every block maximum is one or two shuffles and no warp
 // waits for another before the outputs are staged: the scale bytes in the
 // atoms' order, and the transposed codes as 64-byte lines (16-byte chunks XORed
-// with the column block, two lanes a bank).  HBM bound: per element 2 B read,
-// 1/2 B of codes and 1/32 or 1/16 B of scales written per direction.
+// with the column block, two lanes a bank).  Per element 2 B read, 1/2 B of codes
+// and 1/32 or 1/16 B of scales written per direction: HBM bound in one direction
+// (16384 x 8960: 66 us MXFP4, 69 to 75 us NVFP4, 5.0 to 5.7 TB/s), bound by the code
+// arithmetic in both (93 us and 122 us; 20 instructions an element at 60% of the
+// issue slots).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -42,7 +45,8 @@ constexpr int kStages = 3;
 struct Mx4Ctrl {
   uint64_t full[kStages], empty[kStages];
   int abort;
-  alignas(16) uint8_t atoms[2 * kMx4AtomBytes];       // row scales of a tile
+  alignas(16) float2 divisor[128];                 // NVFP4: (d, -1/d) of every scale byte
+  alignas(16) uint8_t atoms[2 * kMx4AtomBytes];    // row scales of a tile
   alignas(16) uint8_t atoms_t[2 * kMx4AtomBytes];     // column scales
   alignas(16) uint8_t codes_t[kTile * kTile / 2];  // transposed codes: 128 lines of 64 bytes
 };
@@ -85,6 +89,10 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
   griddep_wait();
   if (t == 0) griddep_launch_dependents();
   const float g = kNv && a.tensor_scale ? __ldg(a.tensor_scale) : 1.0f, rg = __frcp_rn(g);
+  if (kNv && t < 128) {                    // read after the first tile's barrier
+    const QScale q = nvfp4_divisor(t, g);
+    ctrl->divisor[t] = make_float2(q.s, q.nr);
+  }
 
   // This thread's 8 x 8: rows 32 (warp / 2) + 8 (lane / 8) .., columns 64 (warp % 2) + 8 (lane % 8) ..
   const int r0 = 32 * (warp >> 1) + 8 * (lane >> 3), bj = lane & 7, c0 = 64 * (warp & 1) + 8 * bj;
@@ -160,13 +168,13 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
         const float lo = __uint_as_float(cm[j] << 16), hi = __uint_as_float(cm[j] & 0xFFFF0000u);
         if constexpr (kNv) {
           const bool odd = lane & 8;
-          QScale q;
-          put(c0 + 2 * j + odd, block_scale<kNv>(odd ? hi : lo, g, rg, q));
-          const float os = __shfl_xor_sync(0xFFFFFFFFu, q.s, 8), on = __shfl_xor_sync(0xFFFFFFFFu, q.nr, 8);
-          cs[2 * j] = odd ? os : q.s;
-          cs[2 * j + 1] = odd ? q.s : os;
-          cn[2 * j] = odd ? on : q.nr;
-          cn[2 * j + 1] = odd ? q.nr : on;
+          const uint32_t byte = nvfp4_scale(odd ? hi : lo, g, rg), other = __shfl_xor_sync(0xFFFFFFFFu, byte, 8);
+          put(c0 + 2 * j + odd, byte);
+          const float2 q0 = ctrl->divisor[odd ? other : byte], q1 = ctrl->divisor[odd ? byte : other];
+          cs[2 * j] = q0.x;
+          cs[2 * j + 1] = q1.x;
+          cn[2 * j] = q0.y;
+          cn[2 * j + 1] = q1.y;
         } else {
           QScale q0, q1;
           const uint32_t b0 = block_scale<kNv>(lo, g, rg, q0), b1 = block_scale<kNv>(hi, g, rg, q1);
@@ -183,7 +191,11 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
 
     // Codes, two rows at a time: a column's values of rows 2p and 2p + 1 form one
     // pair, divided in one packed step by the rows' scales and by the column's.
-    [[maybe_unused]] uint32_t line[8] = {0, 0, 0, 0, 0, 0, 0, 0};   // transposed: this thread's 8 rows of each column
+    // Transposed: of each column, the scaled values of the rows 2p and 2p + 1 for even
+    // p, and the codes of this thread's rows so far, four rows to a half word.
+    [[maybe_unused]] float2 pend[8];
+    [[maybe_unused]] uint16_t half[8];
+    [[maybe_unused]] uint32_t line[8];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       float2 x[8];
@@ -230,18 +242,26 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
           lo8[c] = w.x;
           hi8[c] = w.y;
         }
-        const int64_t row = row0 + r0 + 2 * p;
-        uint8_t* dst = a.q_row + row * (a.cols / 2) + (col0 + c0) / 2;
-        if (col0 + c0 < a.cols) {
-          if (row < a.rows) *reinterpret_cast<uint32_t*>(dst) = cvt8_e2m1(lo8) ^ (kNv ? 0x88888888u : 0u);
-          if (row + 1 < a.rows) *reinterpret_cast<uint32_t*>(dst + a.cols / 2) = cvt8_e2m1(hi8) ^ (kNv ? 0x88888888u : 0u);
-        }
+        // Neighbouring lanes exchange halves: the even lane stores 16 columns of row 2p, the odd one of row 2p + 1.
+        const uint32_t lo_c = cvt8_e2m1(lo8) ^ (kNv ? 0x88888888u : 0u), hi_c = cvt8_e2m1(hi8) ^ (kNv ? 0x88888888u : 0u);
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? lo_c : hi_c, 1);
+        const int64_t row = row0 + r0 + 2 * p + (lane & 1);
+        const int64_t col = col0 + c0 - 8 * (lane & 1);
+        if (row < a.rows && col < a.cols)
+          *reinterpret_cast<uint2*>(a.q_row + row * (a.cols / 2) + col / 2) =
+              (lane & 1) ? make_uint2(got, hi_c) : make_uint2(lo_c, got);
       }
       if constexpr (kColT) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float2 w = scaled2<kNv>(x[c], make_float2(cs[c], cs[c]), make_float2(cn[c], cn[c]));
-          line[c] |= cvt2_e2m1(w.x, w.y) << (8 * p);
+          if ((p & 1) == 0) {
+            pend[c] = w;
+          } else {
+            const uint16_t codes = cvt4_e2m1(pend[c].x, pend[c].y, w.x, w.y);
+            if (p == 1) half[c] = codes;
+            else line[c] = half[c] | (static_cast<uint32_t>(codes) << 16);
+          }
         }
       }
     }
