@@ -492,16 +492,16 @@ def _keep_for(stream, *tensors) -> None:
                 t.record_stream(stream)
 
 
-def fp8blk_linear_grouped_workspace_bytes(rows: int, k: int) -> int:
-    """Bytes of workspace fp8blk_linear_grouped needs for x [rows, k]."""
-    return int(lib.fp8blk_linear_grouped_workspace_bytes(int(rows), int(k)))
+def fp8blk_linear_grouped_workspace_bytes(groups: int, rows: int, k: int) -> int:
+    """Bytes of workspace fp8blk_linear_grouped needs for x [rows, k] in `groups` groups (0: none)."""
+    return int(lib.fp8blk_linear_grouped_workspace_bytes(int(groups), int(rows), int(k)))
 
 
 def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=None, out_dtype=torch.bfloat16):
     """Y[t] = X[t] . W[e]^T for the rows t of group e, x [T,in] bf16 quantised on the way, W [groups,out,in]
     ahead as one weight of groups*out rows (qw, sw): the result of fp8blk_quantize_act_1x128_grouped and
     fp8blk_gemm_grouped, in one launch with up to 16 rows.  workspace: a uint8 CUDA tensor of at least
-    fp8blk_linear_grouped_workspace_bytes(T, in) bytes (allocated here when None)."""
+    fp8blk_linear_grouped_workspace_bytes(groups, T, in) bytes (allocated here when None and needed)."""
     x = _bf16_2d(x)
     groups = _offsets(offsets)
     dev = _need_cuda(x, qw, sw, offsets, d, workspace)
@@ -515,8 +515,9 @@ def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=Non
         raise ValueError("codes and scales must be contiguous")
     made = []
     if workspace is None:
-        workspace = _empty((rows * k + rows * (k // 128) * 4,), torch.uint8, dev)
-        made.append(workspace)
+        if rows > 16 or rows > 12 * groups:    # else one launch, which needs none
+            workspace = _empty((rows * k + rows * (k // 128) * 4,), torch.uint8, dev)
+            made.append(workspace)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     if d is None:
@@ -529,7 +530,8 @@ def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=Non
     pitch, ldx = _pitch(d, n), _pitch(x, k)
     _keep_for(stream, *made)
     _run(dev, lib.fp8blk_linear_grouped, OUT_F32 if d.dtype == torch.float32 else 0, groups, offsets.data_ptr(), rows, n,
-         k, x.data_ptr(), ldx, qw.data_ptr(), sw.data_ptr(), workspace.data_ptr(), workspace.numel(), d.data_ptr(), pitch,
+         k, x.data_ptr(), ldx, qw.data_ptr(), sw.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+         d.data_ptr(), pitch,
          _stream_handle(stream, dev))
     return d
 
@@ -648,7 +650,7 @@ def fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa=None, tensor_sb=None, d=None, s
 
 
 def fp8blk_linear_mx4_workspace_bytes(fmt, m: int, k: int) -> int:
-    """Bytes of workspace fp8blk_linear_mx4 needs for x [m, k]."""
+    """Bytes of workspace fp8blk_linear_mx4 needs for x [m, k] (0 for m <= 16)."""
     return int(lib.fp8blk_linear_mx4_workspace_bytes(int(fmt), int(m), int(k)))
 
 
@@ -656,7 +658,7 @@ def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, wo
                       out_dtype=torch.bfloat16):
     """Y = X . W^T in 4 bits, x [M,K] bf16 quantised on the way, W [N,K] ahead (qw [N,K/2], sw): the result of
     fp8blk_quantize_mx4 and fp8blk_gemm_mx4, in one launch when M <= 16.  workspace: a uint8 CUDA tensor of at
-    least fp8blk_linear_mx4_workspace_bytes(fmt, M, K) bytes (allocated here when None)."""
+    least fp8blk_linear_mx4_workspace_bytes(fmt, M, K) bytes (allocated here when None and needed)."""
     x = _bf16_2d(x)
     if fmt not in MX4_BLOCK:
         raise ValueError("fmt must be MXFP4 or NVFP4")
@@ -667,9 +669,10 @@ def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, wo
         raise ValueError("X and W disagree on their features")
     made = []
     if workspace is None:
-        blocks, atoms, size = _mx4_scale_shape(fmt, m, k)
-        workspace = _empty((-(-m * k // 32) * 16 + blocks * atoms * size,), torch.uint8, dev)
-        made.append(workspace)
+        if m > 16:                             # else one launch, which needs none
+            blocks, atoms, size = _mx4_scale_shape(fmt, m, k)
+            workspace = _empty((-(-m * k // 32) * 16 + blocks * atoms * size,), torch.uint8, dev)
+            made.append(workspace)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     if d is None:
@@ -685,8 +688,8 @@ def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, wo
     pitch, ldx = _pitch(d, -(-n // 8) * 8), _pitch(x, k)
     _keep_for(stream, *made)
     _run(dev, lib.fp8blk_linear_mx4, fmt | (OUT_F32 if d.dtype == torch.float32 else 0), m, n, k, x.data_ptr(), ldx,
-         _ptr(tensor_sx), qw.data_ptr(), sw.data_ptr(), _ptr(tensor_sw), workspace.data_ptr(), workspace.numel(),
-         d.data_ptr(), pitch, _stream_handle(stream, dev))
+         _ptr(tensor_sx), qw.data_ptr(), sw.data_ptr(), _ptr(tensor_sw), _ptr(workspace),
+         0 if workspace is None else workspace.numel(), d.data_ptr(), pitch, _stream_handle(stream, dev))
     return d
 
 

@@ -70,7 +70,7 @@ def _load() -> ctypes.CDLL:
         "fp8blk_linear_mx4": [I, I64, I64, I64, P, I64, P, P, P, P, P, I64, P, I64, P],
         "fp8blk_linear_mx4_workspace_bytes": [I, I64, I64],
         "fp8blk_linear_grouped": [I, I64, P, I64, I64, I64, P, I64, P, P, P, I64, P, I64, P],
-        "fp8blk_linear_grouped_workspace_bytes": [I64, I64],
+        "fp8blk_linear_grouped_workspace_bytes": [I64, I64, I64],
         "fp8blk_gemm_splitk": [I, I64, I64, I64, P, P, P, P, P, I64, I, P, I64, P],
         "fp8blk_gemm_splitk_workspace_bytes": [I, I64, I64, I64, I],
         "fp8blk_gemm_splitk_count": [I, I64, I64, I64],

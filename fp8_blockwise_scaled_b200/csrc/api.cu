@@ -410,9 +410,9 @@ fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* off
   return launch_status(fp8blk::launch_gemm_grouped(g, static_cast<cudaStream_t>(stream)));
 }
 
-int64_t fp8blk_linear_grouped_workspace_bytes(int64_t M, int64_t K) {
-  if (M < 0 || K < 0 || K % 128 != 0) return -1;
-  return M * K + M * (K / 128) * 4;
+int64_t fp8blk_linear_grouped_workspace_bytes(int64_t groups, int64_t M, int64_t K) {
+  if (groups < 1 || groups > FP8BLK_MAX_GROUPS || M < 0 || K < 0 || K % 128 != 0) return -1;
+  return fp8blk::grouped_quantizes_on_the_way(M, groups) ? 0 : M * K + M * (K / 128) * 4;
 }
 
 fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
@@ -426,14 +426,14 @@ fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* o
   // The quantiser's limits (fp8blk_quantize_act_1x128_grouped).
   const int64_t padded = fp8blk_grouped_padded_rows(M, groups);
   if (padded > (int64_t(1) << 25) || (padded / 128 + 1) * (K / 128) >= (int64_t(1) << 31)) return FP8BLK_ERR_SHAPE;
-  if (!x || ldx < K || !workspace) return FP8BLK_ERR_INVALID_ARG;
+  const bool one_launch = fp8blk::grouped_quantizes_on_the_way(M, groups);
+  if (!x || ldx < K || (!workspace && !one_launch)) return FP8BLK_ERR_INVALID_ARG;
   if (!aligned16(x) || ldx % 8 != 0 || !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
-  if (workspace_bytes < fp8blk_linear_grouped_workspace_bytes(M, K)) return FP8BLK_ERR_INVALID_ARG;
+  if (workspace_bytes < fp8blk_linear_grouped_workspace_bytes(groups, M, K)) return FP8BLK_ERR_INVALID_ARG;
   if ((st = grouped_gemm_device(g)) != FP8BLK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint16_t* xv = static_cast<const uint16_t*>(x);
-  if (fp8blk::grouped_quantizes_on_the_way(g))
-    return launch_status(fp8blk::launch_linear_grouped(g, xv, ldx, s));
+  if (one_launch) return launch_status(fp8blk::launch_linear_grouped(g, xv, ldx, s));
   uint8_t* q = static_cast<uint8_t*>(workspace);
   QuantArgs a{xv, M, K, ldx, q, reinterpret_cast<float*>(q + M * K), nullptr, nullptr, padded / 128, K / 128};
   if ((st = set_quant_waits(a)) != FP8BLK_OK) return st;
@@ -636,7 +636,7 @@ fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const
 int64_t fp8blk_linear_mx4_workspace_bytes(int format, int64_t M, int64_t K) {
   const int64_t scales = fp8blk_mx4_scale_bytes(format, M, K);
   if (scales < 0 || K % 32 != 0) return -1;
-  return (M * (K / 2) + 15) / 16 * 16 + scales;
+  return fp8blk::mx4_quantizes_on_the_way(M) ? 0 : (M * (K / 2) + 15) / 16 * 16 + scales;
 }
 
 fp8blk_status fp8blk_linear_mx4(int format, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
@@ -645,7 +645,8 @@ fp8blk_status fp8blk_linear_mx4(int format, int64_t M, int64_t N, int64_t K, con
   fp8blk::Mx4GemmArgs g;
   fp8blk_status st = mx4_gemm_args(format, M, N, K, tensor_sx, w, sw, tensor_sw, d, ldd, g);
   if (st != FP8BLK_OK || M == 0) return st;
-  if (ldx < K || (K > 0 && (!x || !workspace))) return FP8BLK_ERR_INVALID_ARG;
+  const bool one_launch = fp8blk::mx4_quantizes_on_the_way(M);
+  if (ldx < K || (K > 0 && (!x || (!workspace && !one_launch)))) return FP8BLK_ERR_INVALID_ARG;
   if (!aligned16(x) || ldx % 8 != 0 || !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
   const int base = format & ~FP8BLK_OUT_F32;
   if (workspace_bytes < fp8blk_linear_mx4_workspace_bytes(base, M, K)) return FP8BLK_ERR_INVALID_ARG;
@@ -653,7 +654,7 @@ fp8blk_status fp8blk_linear_mx4(int format, int64_t M, int64_t N, int64_t K, con
   if (K == 0) return mx4_zeros(g, stream);
   const uint16_t* xv = static_cast<const uint16_t*>(x);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (fp8blk::mx4_quantizes_on_the_way(M, N, g.max_ctas)) return launch_status(fp8blk::launch_linear_mx4(g, xv, ldx, s));
+  if (one_launch) return launch_status(fp8blk::launch_linear_mx4(g, xv, ldx, s));
   uint8_t* q = static_cast<uint8_t*>(workspace);
   fp8blk::Mx4QuantArgs a{};
   a.x = xv;

@@ -865,8 +865,13 @@ cudaError_t launch_grouped_few(const GroupedGemmArgs& g, const FewInput& in, cud
 
 namespace {
 
+// Up to 12 rows a group on average go to gemm_grouped_few_kernel; measured with 64
+// groups of 2560 x 1536: 8 rows 44.4 us against 50.5 us (128-row tiles), 12 rows 44.7
+// to 47.8 us (evenly spread to skewed) against 50.7, 16 rows 50.3 to 51.2 against 50.9.
+constexpr int64_t kFewRowsPerGroup = 12;
+
 bool grouped_few_rows(const GroupedGemmArgs& g) {
-  return g.layout != 2 && g.block_n == 0 && g.rows <= 12 * g.groups;
+  return g.layout != 2 && g.block_n == 0 && g.rows <= kFewRowsPerGroup * g.groups;
 }
 
 }  // namespace
@@ -875,7 +880,7 @@ bool grouped_few_rows(const GroupedGemmArgs& g) {
 // 8 rows 11.8 us against 12.8 us for the two launches, 16 rows 17.7 against 17.1,
 // 64 rows 44.4 against 41.0 (the fence between the codes and the tensor cores' reads
 // waits for the loads ahead of it, so every K-block waits for L2).
-bool grouped_quantizes_on_the_way(const GroupedGemmArgs& g) { return g.rows <= 16 && grouped_few_rows(g); }
+bool grouped_quantizes_on_the_way(int64_t rows, int64_t groups) { return rows <= 16 && rows <= kFewRowsPerGroup * groups; }
 
 cudaError_t launch_linear_grouped(const GroupedGemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream) {
   return launch_grouped_few<true>(g, FewInput{x, ldx}, stream);
@@ -883,9 +888,6 @@ cudaError_t launch_linear_grouped(const GroupedGemmArgs& g, const uint16_t* x, i
 
 cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, cudaStream_t stream) {
   const bool wgrad = g.layout == 2;
-  // Up to 12 rows a group on average; measured with 64 groups of 2560 x 1536: 8 rows
-  // 46.1 us against 49.5 us (128-row tiles), 16 rows 47.6 to 52.7 us (evenly spread to
-  // skewed) against 50.1 us.
   if (grouped_few_rows(g)) return launch_grouped_few<false>(g, {}, stream);
   // 256-column tiles, unless even the most tiles that the rows can make leave SMs
   // idle (64 groups of 2560 x 1536, 1024 to 24576 rows: within 4% of 128-column

@@ -135,8 +135,8 @@ struct GroupedGemmArgs {
 cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, cudaStream_t stream);
 
 // FWD with A quantised on the way from x [T][ldx] bf16 (g.a and g.sa unused): one
-// launch, where grouped_quantizes_on_the_way(g).
-bool grouped_quantizes_on_the_way(const GroupedGemmArgs& g);
+// launch, where grouped_quantizes_on_the_way(T, groups).
+bool grouped_quantizes_on_the_way(int64_t rows, int64_t groups);
 cudaError_t launch_linear_grouped(const GroupedGemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream);
 
 // 4-bit microscaled quantisation (mx4_quant.cu) and products (mx4_gemm.cu).
@@ -192,7 +192,7 @@ cudaError_t launch_gemm_mx4(const Mx4GemmArgs& g, cudaStream_t stream);
 
 // The product with a quantised on the way from x [M][ldx] bf16 (g.a and g.sa
 // unused): one launch, for the few rows that mx4_quantizes_on_the_way allows.
-bool mx4_quantizes_on_the_way(int64_t M, int64_t N, int max_ctas);
+bool mx4_quantizes_on_the_way(int64_t M);
 cudaError_t launch_linear_mx4(const Mx4GemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream);
 
 // y[i] = bf16_round_nearest_even(x[i]) for i < n (x, y 16-byte aligned).

@@ -1028,6 +1028,8 @@ cudaError_t launch_mx4_pair(const Mx4GemmArgs& g, cudaStream_t stream) {
 
 template <bool kNv>
 cudaError_t launch_mx4_fmt(const Mx4GemmArgs& g, cudaStream_t stream) {
+  // Up to 64 rows: 17920 x 8960 NVFP4 with 16 rows 14.5 us (128 x 128 tiles: 24.8), with 64 rows 17.5 (22.0); 8960 x
+  // 4096 with 64 rows 10.2 (11.5).
   if (g.M <= 16) return launch_mx4_few<16, kNv, false>(g, {}, stream);
   if (g.M <= 32) return launch_mx4_few<32, kNv, false>(g, {}, stream);
   if (g.M <= 64) return launch_mx4_few<64, kNv, false>(g, {}, stream);
@@ -1040,10 +1042,9 @@ cudaError_t launch_mx4_fmt(const Mx4GemmArgs& g, cudaStream_t stream) {
 
 }  // namespace
 
-bool mx4_quantizes_on_the_way(int64_t M, int64_t N, int max_ctas) {
-  // Without a cap on the CTAs (the kernel is not persistent).
-  return M <= 16 && (max_ctas <= 0 || (N + 127) / 128 * 8 <= max_ctas);
-}
+// Few rows: 1 x 1536 x 8960 9.7 us for the two launches, 7.3 us in one; 16 x 17920 x
+// 8960 the same either way.
+bool mx4_quantizes_on_the_way(int64_t M) { return M <= 16; }
 
 cudaError_t launch_linear_mx4(const Mx4GemmArgs& g, const uint16_t* x, int64_t ldx, cudaStream_t stream) {
   const FewInput in{x, ldx};

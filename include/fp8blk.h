@@ -52,7 +52,8 @@
  *      FP8BLK_GEMM_SPLITK=0       fp8blk_gemm_splitk_count returns 1 (no split)
  *      FP8BLK_GEMM_MAX_CTAS       at most this many GEMM CTAs (one per SM), so
  *                                 that concurrent work on other streams finds
- *                                 free SMs (default: one per SM)
+ *                                 free SMs (default: one per SM; not kept by
+ *                                 fp8blk_linear_mx4 with M <= 16)
  *      FP8BLK_QUANT_MAX_CTAS      the same for the quantisers (default: as many
  *                                 as fit, two per SM)
  *      FP8BLK_TEST_INJECT_STALL=1 tests only: one wait of the next launch
@@ -286,13 +287,15 @@ fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* off
  * a group on average) it is one launch that leaves the workspace unused, else
  * those two.
  *   format      0, or FP8BLK_OUT_F32.
- *   workspace   device memory of at least fp8blk_linear_grouped_workspace_bytes(M, K)
- *               bytes, 16-byte aligned, owned by the caller, overwritten; two calls
- *               may share it only if they are ordered (one stream, or events).
- * Other arguments and errors as for those two calls; the size is -1 for a
- * negative M or K no multiple of 128.
+ *   workspace   device memory of at least
+ *               fp8blk_linear_grouped_workspace_bytes(groups, M, K) bytes (0, and
+ *               null allowed, where it is one launch), 16-byte aligned, owned by the
+ *               caller, overwritten; two calls may share it only if they are ordered
+ *               (one stream, or events).
+ * Other arguments and errors as for those two calls; the size is -1 for groups out
+ * of range, a negative M or K no multiple of 128.
  */
-int64_t fp8blk_linear_grouped_workspace_bytes(int64_t M, int64_t K);
+int64_t fp8blk_linear_grouped_workspace_bytes(int64_t groups, int64_t M, int64_t K);
 fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
                                     const void* x, int64_t ldx, const uint8_t* w, const float* sw, void* workspace,
                                     int64_t workspace_bytes, void* d, int64_t ldd, void* stream);
@@ -424,9 +427,10 @@ fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const
  * with (w, sw).  With M <= 16 it is one launch that leaves the workspace
  * unused, else those two.
  *   workspace   device memory of at least
- *               fp8blk_linear_mx4_workspace_bytes(format, M, K) bytes, 16-byte
- *               aligned, owned by the caller, overwritten; two calls may share
- *               it only if they are ordered (one stream, or events).
+ *               fp8blk_linear_mx4_workspace_bytes(format, M, K) bytes (0, and null
+ *               allowed, for M <= 16), 16-byte aligned, owned by the caller,
+ *               overwritten; two calls may share it only if they are ordered
+ *               (one stream, or events).
  * Other arguments and errors as for those two calls (K a multiple of 32); the
  * size is -1 for a bad format, a negative size or K no multiple of 32 (format
  * without FP8BLK_OUT_F32).

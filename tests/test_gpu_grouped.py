@@ -408,7 +408,7 @@ def test_quantised_on_the_way_is_the_two_calls(counts, n, k, out_dtype):
     want = torch.full((rows, n), 7.0, dtype=out_dtype, device="cuda")
     q, s, _, _ = fb.fp8blk_quantize_act_1x128_grouped(x, off)
     fb.fp8blk_gemm_grouped(fb.FWD, q, s, QW, SW, off, d=want)
-    size = fb.fp8blk_linear_grouped_workspace_bytes(rows, k)
+    size = fb.fp8blk_linear_grouped_workspace_bytes(len(counts), rows, k)
     work = torch.full((size + 64,), 0x55, dtype=torch.uint8, device="cuda")
     wide = torch.full((rows, n + 32), 7.0, dtype=out_dtype, device="cuda")
     got = fb.fp8blk_linear_grouped(x, QW, SW, off, d=wide[:, :n], workspace=work[:size])

@@ -348,17 +348,17 @@ def test_quantised_on_the_way_is_the_two_calls(m, n, k, fmt, gx, gw, out_dtype):
     assert bool((work[size:] == 0x55).all()) and bool((wide[m:] == 7.0).all()) and bool((wide[:, n:] == 7.0).all())
 
 
-def test_quantised_on_the_way_under_a_cap_on_the_ctas(monkeypatch):
-    """With few CTAs allowed the two launches run instead; the same values but for the order of the sums."""
+def test_few_rows_under_a_cap_on_the_ctas(monkeypatch):
+    """With few CTAs allowed another kernel runs; the same values but for the order of the sums."""
     require_cuda()
     x, w = to_dev(_x(5, 1536, 1, False)), to_dev(_x(640, 1536, 2, False))
-    qw, sw, _, _ = fb.fp8blk_quantize_mx4(w, fb.NVFP4)
-    want = fb.fp8blk_linear_mx4(x, qw, sw, fb.NVFP4, out_dtype=torch.float32)
+    (qx, sx, _, _), (qw, sw, _, _) = fb.fp8blk_quantize_mx4(x, fb.NVFP4), fb.fp8blk_quantize_mx4(w, fb.NVFP4)
+    want = fb.fp8blk_gemm_mx4(qx, sx, qw, sw, fb.NVFP4, out_dtype=torch.float32)
     monkeypatch.setenv("FP8BLK_GEMM_MAX_CTAS", "3")
-    got = fb.fp8blk_linear_mx4(x, qw, sw, fb.NVFP4, out_dtype=torch.float32)
+    got = fb.fp8blk_gemm_mx4(qx, sx, qw, sw, fb.NVFP4, out_dtype=torch.float32)
     assert fb.fp8blk_get_device_error() == 0
     # Sums of 1536 exact products in fp32, in two orders: each within 1536 2^-24 and 24 steps' 2^-21 of the sum of magnitudes.
-    a, b = (fb.fp8blk_dequantize_mx4(*fb.fp8blk_quantize_mx4(t, fb.NVFP4)[:2], fb.NVFP4).double().abs() for t in (x, w))
+    a, b = (fb.fp8blk_dequantize_mx4(*t, fb.NVFP4).double().abs() for t in ((qx, sx), (qw, sw)))
     bound = 2 * (24 * 2.0**-21 + 1536 * 2.0**-24) * (a @ b.t())
     assert bool(((got.double() - want.double()).abs() <= bound).all())
 

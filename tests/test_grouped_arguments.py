@@ -90,9 +90,10 @@ def test_gemm_argument_errors(args, code):
     ((0, 2, A, 5, 128, 128, A, 64, A, A, A, 1 << 20, A, 128, S), 1),       # ldx < K
     ((0, 2, A, 5, 128, 128, A, 132, A, A, A, 1 << 20, A, 128, S), 3),
     ((0, 2, A, 5, 128, 128, MISALIGNED, 128, A, A, A, 1 << 20, A, 128, S), 3),
-    ((0, 2, A, 5, 128, 128, A, 128, A, A, NULL, 1 << 20, A, 128, S), 1),   # no workspace
+    ((0, 2, A, 17, 128, 128, A, 128, A, A, NULL, 1 << 20, A, 128, S), 1),  # no workspace
+    ((0, 1, A, 13, 128, 128, A, 128, A, A, NULL, 1 << 20, A, 128, S), 1),
     ((0, 2, A, 5, 128, 128, A, 128, A, A, MISALIGNED, 1 << 20, A, 128, S), 3),
-    ((0, 2, A, 5, 128, 128, A, 128, A, A, A, 5 * 132 - 1, A, 128, S), 1),  # too small
+    ((0, 2, A, 25, 128, 128, A, 128, A, A, A, 25 * 132 - 1, A, 128, S), 1),  # too small
     ((0, 2, A, 5, 128, 128, A, 128, A, A, A, 1 << 20, A, 64, S), 1),       # ldd < N
     ((0, 2, A, 0, 128, 128, NULL, 128, A, A, NULL, 0, NULL, 128, S), 0),   # nothing to do
 ])
@@ -102,7 +103,8 @@ def test_linear_argument_errors(args, code):
 
 def test_linear_workspace():
     f = fb.fp8blk_linear_grouped_workspace_bytes
-    assert f(5, 256) == 5 * 256 + 5 * 2 * 4 and f(0, 128) == 0 and f(-1, 128) == -1 and f(5, 100) == -1
+    assert f(2, 25, 256) == 25 * 256 + 25 * 2 * 4 and f(2, 0, 128) == 0 and f(2, 16, 128) == 0 and f(1, 12, 128) == 0
+    assert f(1, 13, 128) == 13 * 132 and f(2, -1, 128) == -1 and f(2, 5, 100) == -1 and f(0, 5, 128) == -1
 
 
 def test_calls_without_rows_need_no_gpu():

@@ -113,9 +113,9 @@ def test_gemm_argument_errors(args, code):
     ((0, 5, 8, 32, A, 36, N0, A, A, N0, A, 1 << 20, A, 8, N0), 3),
     ((0, 5, 8, 32, M8, 32, N0, A, A, N0, A, 1 << 20, A, 8, N0), 3),
     ((0, 5, 8, 32, N0, 32, N0, A, A, N0, A, 1 << 20, A, 8, N0), 1),
-    ((0, 5, 8, 32, A, 32, N0, A, A, N0, N0, 1 << 20, A, 8, N0), 1),     # no workspace
+    ((0, 17, 8, 32, A, 32, N0, A, A, N0, N0, 1 << 20, A, 8, N0), 1),    # no workspace
     ((0, 5, 8, 32, A, 32, N0, A, A, N0, M8, 1 << 20, A, 8, N0), 3),
-    ((0, 5, 8, 32, A, 32, N0, A, A, N0, A, 5 * 16 + 511, A, 8, N0), 1), # too small
+    ((0, 17, 8, 32, A, 32, N0, A, A, N0, A, 17 * 16 + 511, A, 8, N0), 1),   # too small
     ((0, 5, 8, 32, A, 32, N0, A, A, N0, A, 1 << 20, A, 4, N0), 1),      # ldd < N
     ((0, 0, 8, 32, N0, 32, N0, A, A, N0, N0, 0, N0, 8, N0), 0),         # nothing to do
 ])
@@ -125,7 +125,7 @@ def test_linear_argument_errors(args, code):
 
 def test_linear_workspace():
     f = fb.fp8blk_linear_mx4_workspace_bytes
-    assert f(fb.MXFP4, 5, 32) == 80 + 512 and f(fb.NVFP4, 129, 96) == 129 * 48 + 2 * 2 * 512
+    assert f(fb.MXFP4, 17, 32) == 17 * 16 + 512 and f(fb.MXFP4, 16, 32) == 0 and f(fb.NVFP4, 129, 96) == 129 * 48 + 2 * 2 * 512
     assert f(2, 5, 32) == -1 and f(fb.MXFP4, -1, 32) == -1 and f(fb.MXFP4, 5, 48) == -1 and f(fb.MXFP4, 0, 32) == 0
 
 
