@@ -481,15 +481,20 @@ def fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, d=None, stream=None, out_
     return d
 
 
-def _keep_for(stream, *tensors) -> None:
-    """Tensors made here and used on a `stream` that was passed in: their memory is not given out again
-    before the work on it is done (without a stream they belong to the current one, as the work does)."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=tensors[0].device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _on_stream(stream, device, call):
+    """call() with `stream` current: what it allocates is that stream's memory, which no earlier work of
+    another stream still uses, and its results' memory is not given out again before the work that the
+    caller's current stream has for them is done."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = call()
+    for t in out if isinstance(out, tuple) else (out,):
+        t.record_stream(caller)
+    return out
 
 
 def fp8blk_linear_grouped_workspace_bytes(groups: int, rows: int, k: int) -> int:
@@ -505,6 +510,9 @@ def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=Non
     x = _bf16_2d(x)
     groups = _offsets(offsets)
     dev = _need_cuda(x, qw, sw, offsets, d, workspace)
+    if stream is not None and (d is None or workspace is None):
+        return _on_stream(stream, dev,
+                          lambda: fp8blk_linear_grouped(x, qw, sw, offsets, d, workspace, None, out_dtype))
     rows, k = x.shape
     n = qw.shape[0] // groups
     if qw.dtype != E4M3 or sw.dtype != torch.float32:
@@ -513,22 +521,18 @@ def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=Non
         raise ValueError(f"weight {tuple(qw.shape)}, {tuple(sw.shape)} does not match X {tuple(x.shape)} and {groups} groups")
     if not (qw.is_contiguous() and sw.is_contiguous()):
         raise ValueError("codes and scales must be contiguous")
-    made = []
     if workspace is None:
         if rows > 16 or rows > 12 * groups:    # else one launch, which needs none
             workspace = _empty((rows * k + rows * (k // 128) * 4,), torch.uint8, dev)
-            made.append(workspace)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     if d is None:
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
         d = _empty((rows, n), out_dtype, dev)
-        made.append(d)
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (rows, n) or d.stride(1) != 1:
         raise ValueError(f"d must be a bfloat16 or float32 {(rows, n)} tensor with unit column stride")
     pitch, ldx = _pitch(d, n), _pitch(x, k)
-    _keep_for(stream, *made)
     _run(dev, lib.fp8blk_linear_grouped, OUT_F32 if d.dtype == torch.float32 else 0, groups, offsets.data_ptr(), rows, n,
          k, x.data_ptr(), ldx, qw.data_ptr(), sw.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(),
          d.data_ptr(), pitch,
@@ -545,11 +549,13 @@ def grouped_linear_forward(x, qw, sw, offsets, stream=None):
 def grouped_linear_backward(x, dy, qwT, swT, offsets, stream=None, out_dtype=torch.bfloat16):
     """(dX [T,in], dW [groups,out,in]) of grouped_linear_forward, both FP8 blockwise; the transposed weights
     come quantised (fp8blk_quantize_weight_128x128_t or _both: qwT [in,groups*out], swT).  out_dtype: dW's."""
-    qdy, sdy, qdyT, sdyT = fp8blk_quantize_act_1x128_grouped(dy, offsets, BOTH, stream=stream)
-    _, _, qxT, sxT = fp8blk_quantize_act_1x128_grouped(x, offsets, COLWISE_T, stream=stream)
-    dx = fp8blk_gemm_grouped(DGRAD, qdy, sdy, qwT, swT, offsets, stream=stream)
-    dw = fp8blk_gemm_grouped(WGRAD, qdyT, sdyT, qxT, sxT, offsets, stream=stream, out_dtype=out_dtype)
-    _keep_for(stream, qdy, sdy, qdyT, sdyT, qxT, sxT, dx, dw)
+    if stream is not None:
+        return _on_stream(stream, _need_cuda(x, dy),
+                          lambda: grouped_linear_backward(x, dy, qwT, swT, offsets, None, out_dtype))
+    qdy, sdy, qdyT, sdyT = fp8blk_quantize_act_1x128_grouped(dy, offsets, BOTH)
+    _, _, qxT, sxT = fp8blk_quantize_act_1x128_grouped(x, offsets, COLWISE_T)
+    dx = fp8blk_gemm_grouped(DGRAD, qdy, sdy, qwT, swT, offsets)
+    dw = fp8blk_gemm_grouped(WGRAD, qdyT, sdyT, qxT, sxT, offsets, out_dtype=out_dtype)
     return dx, dw
 
 
@@ -664,15 +670,16 @@ def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, wo
         raise ValueError("fmt must be MXFP4 or NVFP4")
     dev = _need_cuda(x, qw, sw, _tensor_scale(tensor_sx), _tensor_scale(tensor_sw), d, workspace)
     n, k = _mx4_operand(qw, sw, fmt, "W")
+    if stream is not None and (d is None or workspace is None):
+        return _on_stream(stream, dev, lambda: fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx, tensor_sw, d, workspace,
+                                                                 None, out_dtype))
     m = x.shape[0]
     if x.shape[1] != k:
         raise ValueError("X and W disagree on their features")
-    made = []
     if workspace is None:
         if m > 16:                             # else one launch, which needs none
             blocks, atoms, size = _mx4_scale_shape(fmt, m, k)
             workspace = _empty((-(-m * k // 32) * 16 + blocks * atoms * size,), torch.uint8, dev)
-            made.append(workspace)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     if d is None:
@@ -682,11 +689,9 @@ def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, wo
         d = _empty((m, pitch), out_dtype, dev)
         if pitch != n:
             d = d[:, :n]
-        made.append(d)
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (m, n) or d.stride(1) != 1:
         raise ValueError("d must be a bfloat16 or float32 [M,N] tensor with unit column stride")
     pitch, ldx = _pitch(d, -(-n // 8) * 8), _pitch(x, k)
-    _keep_for(stream, *made)
     _run(dev, lib.fp8blk_linear_mx4, fmt | (OUT_F32 if d.dtype == torch.float32 else 0), m, n, k, x.data_ptr(), ldx,
          _ptr(tensor_sx), qw.data_ptr(), sw.data_ptr(), _ptr(tensor_sw), _ptr(workspace),
          0 if workspace is None else workspace.numel(), d.data_ptr(), pitch, _stream_handle(stream, dev))
@@ -708,6 +713,8 @@ def mx4_linear_wgrad(x, dy, fmt, x_scale=None, dy_scale=None, stream=None, out_d
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
     dev = _need_cuda(x, dy, _tensor_scale(x_scale), _tensor_scale(dy_scale))
+    if stream is not None:
+        return _on_stream(stream, dev, lambda: mx4_linear_wgrad(x, dy, fmt, x_scale, dy_scale, None, out_dtype))
     tokens, k = x.shape
     n = dy.shape[1]
     if dy.shape[0] != tokens:
@@ -721,8 +728,7 @@ def mx4_linear_wgrad(x, dy, fmt, x_scale=None, dy_scale=None, stream=None, out_d
     work = _empty((at,), torch.uint8, dev)
     pitch = -(-k // 8) * 8
     dw = _empty((n, pitch), out_dtype, dev)
-    _keep_for(stream, work, dw)
-    base, handle, gx, gd = work.data_ptr(), _stream_handle(stream, dev), _ptr(x_scale), _ptr(dy_scale)
+    base, handle, gx, gd = work.data_ptr(), _stream_handle(None, dev), _ptr(x_scale), _ptr(dy_scale)
     qd, sd, qx, sx = (base + p for p in places) if tokens else (None,) * 4
     _run(dev, lib.fp8blk_quantize_mx4, dy.data_ptr(), tokens, n, _pitch(dy, n), COLWISE_T, fmt, gd, None, None, qd, sd, handle)
     _run(dev, lib.fp8blk_quantize_mx4, x.data_ptr(), tokens, k, _pitch(x, k), COLWISE_T, fmt, gx, None, None, qx, sx, handle)
@@ -735,9 +741,11 @@ def mx4_linear_backward(x, dy, qwT, swT, fmt, x_scale=None, dy_scale=None, w_sca
                         out_dtype=torch.bfloat16):
     """(dX, dW) of Y = X . W^T in 4 bits: dY quantised once along features and along tokens, X along
     tokens, W ahead (fp8blk_quantize_mx4, COLWISE_T).  out_dtype: dW's."""
-    qd, sd, qdT, sdT = fp8blk_quantize_mx4(dy, fmt, BOTH, dy_scale, stream=stream)
-    _, _, qxT, sxT = fp8blk_quantize_mx4(x, fmt, COLWISE_T, x_scale, stream=stream)
-    dx = fp8blk_gemm_mx4(qd, sd, qwT, swT, fmt, dy_scale, w_scale, stream=stream)
-    dw = fp8blk_gemm_mx4(qdT, sdT, qxT, sxT, fmt, dy_scale, x_scale, stream=stream, out_dtype=out_dtype)
-    _keep_for(stream, qd, sd, qdT, sdT, qxT, sxT, dx, dw)
+    if stream is not None:
+        return _on_stream(stream, _need_cuda(x, dy), lambda: mx4_linear_backward(x, dy, qwT, swT, fmt, x_scale, dy_scale,
+                                                                                 w_scale, None, out_dtype))
+    qd, sd, qdT, sdT = fp8blk_quantize_mx4(dy, fmt, BOTH, dy_scale)
+    _, _, qxT, sxT = fp8blk_quantize_mx4(x, fmt, COLWISE_T, x_scale)
+    dx = fp8blk_gemm_mx4(qd, sd, qwT, swT, fmt, dy_scale, w_scale)
+    dw = fp8blk_gemm_mx4(qdT, sdT, qxT, sxT, fmt, dy_scale, x_scale, out_dtype=out_dtype)
     return dx, dw

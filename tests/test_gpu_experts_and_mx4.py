@@ -288,3 +288,46 @@ def test_block_codes_match_the_quantisers_used_apart():
     for s, t in zip(a, b):
         s, t = u8(s), u8(t)
         assert np.array_equal(s, t[tuple(slice(0, n) for n in s.shape)])
+
+
+@pytest.mark.parametrize("name", ["grouped_forward", "grouped_few", "grouped_backward", "mx4_forward", "mx4_few",
+                                  "mx4_wgrad", "mx4_backward"])
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_stream_argument_allocates_from_that_stream(name, as_handle):
+    """With `stream` given, nothing that the call allocates may be memory that earlier work of the current
+    stream still writes: blocks of every size, freed behind a long queue of writes of NaN, are not handed to it."""
+    require_cuda()
+    block = Block(3, fb.NVFP4)
+    order, _, ends = _route(4, (2,))
+    token = torch.from_numpy(order // CHOICES).cuda()
+    off = torch.from_numpy(ends.astype(np.int32)).cuda()
+    x, dy = to_dev(block.x), to_dev(block.dy)
+    xs, dys, few = x[token].contiguous(), dy[token].contiguous(), off.clamp(max=9)
+    sc = block.scale
+    call = {
+        "grouped_forward": lambda **k: fb.grouped_linear_forward(xs, block.qw, block.sw, off, **k),
+        "grouped_few": lambda **k: fb.grouped_linear_forward(xs[:9], block.qw, block.sw, few, **k),
+        "grouped_backward": lambda **k: fb.grouped_linear_backward(xs, dys, block.qwT, block.swT, off, **k),
+        "mx4_forward": lambda **k: fb.mx4_linear_forward(x, block.qv, block.sv, block.fmt, sc["x"], sc["v"], **k),
+        "mx4_few": lambda **k: fb.mx4_linear_forward(x[:9], block.qv, block.sv, block.fmt, sc["x"], sc["v"], **k),
+        "mx4_wgrad": lambda **k: fb.mx4_linear_wgrad(x, dy, block.fmt, sc["x"], sc["dy"], **k),
+        "mx4_backward": lambda **k: fb.mx4_linear_backward(x, dy, block.qvT, block.svT, block.fmt, sc["x"], sc["dy"],
+                                                           sc["v"], **k),
+    }[name]
+    want = call()
+    want = want if isinstance(want, tuple) else (want,)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    blocks = [torch.empty(1 << b, dtype=torch.uint8, device="cuda") for b in range(9, 24) for _ in range(3)]
+    for _ in range(40):
+        for b in blocks:
+            b.fill_(255)
+    taken = [(b.data_ptr(), b.data_ptr() + b.numel()) for b in blocks]
+    del blocks, b
+    got = call(stream=side.cuda_stream if as_handle else side)
+    got = got if isinstance(got, tuple) else (got,)
+    torch.cuda.synchronize()
+    assert fb.fp8blk_get_device_error() == 0
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+        assert not any(lo <= g.data_ptr() < hi for lo, hi in taken)
