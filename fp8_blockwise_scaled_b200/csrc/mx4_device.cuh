@@ -76,12 +76,13 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
 // and rg = RN(1 / g): the tensor's scale.  amax / 6 and that by g are correctly
 // rounded by Markstein's correction, as x / s in qmath.cuh: q0 = RN(a y) with y
 // the correctly rounded reciprocal, then RN(q0 + RN(a - q0 b) y).
-// The scale byte of an NVFP4 block of maximum amax.
+// The scale byte of an NVFP4 block of maximum amax.  Below 128 whatever g holds (a
+// scale has no sign, and the byte is an index into a table of 128).
 __device__ __forceinline__ uint32_t nvfp4_scale(float amax, float g, float rg) {
   constexpr float kSixth = 0x1.555556p-3f;              // RN(1 / 6)
   const float a0 = amax * kSixth, a = fmaf(fmaf(-6.0f, a0, amax), kSixth, a0);
   const float t0 = a * rg, t = fmaf(fmaf(-g, t0, a), rg, t0);
-  return cvt_e4m3(t);
+  return cvt_e4m3(t) & 0x7Fu;
 }
 
 // What the values of an NVFP4 block with that scale byte are divided by.

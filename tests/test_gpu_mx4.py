@@ -377,3 +377,14 @@ def test_stalled_product_that_quantises_reports_timeout_and_recovers(fmt, monkey
     monkeypatch.delenv("FP8BLK_TEST_INJECT_STALL")
     assert torch.equal(fb.fp8blk_linear_mx4(x, qw, sw, FORMATS[fmt]), want)
     assert fb.fp8blk_get_device_error() == 0
+
+
+@pytest.mark.parametrize("g", [-1.0, -0.0, 0.0, float("nan"), float("inf"), -float("inf")])
+def test_tensor_scales_that_are_not_positive_give_bytes_in_range(g):
+    """The device holds the scalar, so the host cannot refuse it: codes are unspecified, scale bytes have no sign."""
+    require_cuda()
+    x = torch.linspace(-3, 3, 160 * 96, device="cuda").reshape(160, 96).bfloat16()
+    _, s, _, sT = fb.fp8blk_quantize_mx4(x, fb.NVFP4, fb.BOTH, tensor_scale=_scalar(g))
+    _, s1, _, _ = fb.fp8blk_quantize_mx4(x, fb.NVFP4, fb.ROWWISE, tensor_scale=_scalar(g))
+    assert int(s.max()) < 128 and int(sT.max()) < 128 and torch.equal(s, s1)
+    assert fb.fp8blk_get_device_error() == 0
