@@ -331,3 +331,38 @@ def test_stream_argument_allocates_from_that_stream(name, as_handle):
     for g, w in zip(got, want):
         assert torch.equal(g, w)
         assert not any(lo <= g.data_ptr() < hi for lo, hi in taken)
+
+
+def test_stream_argument_inside_a_capture():
+    """A side stream that joins a capture, given as an argument: the graph replays with new inputs."""
+    require_cuda()
+    block = Block(3, fb.MXFP4)
+    order, _, ends = _route(4, (2,))
+    token = torch.from_numpy(order // CHOICES).cuda()
+    off = torch.from_numpy(ends.astype(np.int32)).cuda()
+    x, dy = to_dev(block.x)[token].contiguous(), to_dev(block.dy)[token].contiguous()
+    xf = to_dev(block.x)
+
+    def run(**k):
+        return (fb.grouped_linear_forward(x, block.qw, block.sw, off, **k),
+                *fb.grouped_linear_backward(x, dy, block.qwT, block.swT, off, **k),
+                fb.mx4_linear_forward(xf, block.qv, block.sv, block.fmt, **k),
+                fb.mx4_linear_wgrad(x, dy, block.fmt, **k))
+
+    run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = run(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for scale in (1.0, -0.5):
+        x.mul_(scale)
+        dy.mul_(scale)
+        xf.mul_(scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(out, run()):
+            assert torch.equal(got, want)
+    assert fb.fp8blk_get_device_error() == 0
