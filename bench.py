@@ -53,8 +53,8 @@ L2_FLUSH_BYTES = 256 << 20
 # one step; profiles/gemm_dram_layer_16384.md); algorithmic minimum 2.59 GB (codes
 # read once, bf16 outputs written once).  It describes the GEMM source whose
 # SHA-256 prefix is given; for any other source the bench reports no traffic.
-GEMM_STEP_DRAM = {"bytes": 2.881e9, "gemm_cu_sha256": "56f0202c9d77f700"}
-GEMM_SOURCE = os.path.join(ROOT, "fp8_blockwise_scaled_b200", "csrc", "gemm.cu")
+GEMM_STEP_DRAM = {"bytes": 2.911e9, "gemm_sha256": "1eb35993113cfc2c"}
+GEMM_SOURCES = [os.path.join(ROOT, "fp8_blockwise_scaled_b200", "csrc", f) for f in ("gemm.cu", "gemm_device.cuh")]
 
 WORKLOAD_DESC = {
     "layer": "qwen2-1.5b-shaped decoder layer linears (qkv 2048x1536, o 1536x1536, gate_up 17920x1536, "
@@ -75,8 +75,11 @@ def load_peaks() -> tuple[dict, str]:
 
 def gemm_source_sha() -> str:
     import hashlib
-    with open(GEMM_SOURCE, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+    digest = hashlib.sha256()
+    for path in GEMM_SOURCES:
+        with open(path, "rb") as f:
+            digest.update(f.read())
+    return digest.hexdigest()[:16]
 
 
 def fp8_peaks(peaks: dict) -> dict:
@@ -738,7 +741,7 @@ def run_ours(args, rank: int, world: int, local_rank: int):
                          "frac": round(rate / (fp8_peak if kind == "gemm" else peaks["hbm_gbs"]), 3)}
         if prog.splits.get(label, 1) > 1:
             per_op[label]["split_k"] = prog.splits[label]
-    traffic_ok = args.workload == "layer" and tokens == 16384 and gemm_source_sha() == GEMM_STEP_DRAM["gemm_cu_sha256"]
+    traffic_ok = args.workload == "layer" and tokens == 16384 and gemm_source_sha() == GEMM_STEP_DRAM["gemm_sha256"]
     extra = {}
     if rank == 0 and world == 1 and args.workload == "layer" and not args.no_extra:
         extra["configs_8192"] = time_configs_8192(dev, flush, fp8, max(3, min(args.steps, 10)))
