@@ -486,7 +486,10 @@ def _on_stream(stream, device, call):
     another stream still uses, and its results' memory is not given out again before the work that the
     caller's current stream has for them is done."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # Handles 0 and 1 are the legacy default stream (NULL and cudaStreamLegacy).  ExternalStream would take 0 for
+        # "no handle given" and make a stream of its own, and 1 for an identifier of its own streams.
+        handle = int(stream)
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=device)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     caller = torch.cuda.current_stream(device)

@@ -1,0 +1,65 @@
+"""Calls with a `stream` argument: order on the stream that is named, and memory that belongs to it."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_blockwise_scaled_b200 as fb
+import workloads
+from tests.gpu_helpers import require_cuda, to_dev
+
+pytestmark = pytest.mark.gpu
+
+T, K, N, GROUPS = 256, 256, 384, 2
+
+
+def _x(rows, cols, seed):
+    return to_dev(workloads.activation(np.random.default_rng(seed), rows, cols))
+
+
+class Case:
+    """Inputs of every entry point that takes a stream, and those calls."""
+
+    def __init__(self):
+        self.x, self.dy, self.w = _x(T, K, 1), _x(T, N, 2), _x(N, K, 3)
+        self.off = torch.tensor([0, 100, T], dtype=torch.int32, device="cuda")
+        self.few = self.off.clamp(max=9)
+        self.one = torch.tensor([0.01], device="cuda")
+        w2 = torch.cat([self.w, self.w])
+        self.qw, self.sw, self.qwT, self.swT = fb.fp8blk_quantize_weight_128x128_both(w2)
+        self.q4, self.s4, self.q4T, self.s4T = fb.fp8blk_quantize_mx4(self.w, fb.MXFP4, fb.BOTH)
+        self.qx, self.sx, _, _ = fb.fp8blk_quantize_act_1x128(self.x)
+        self.q1, self.s1 = fb.fp8blk_quantize_weight_128x128(self.w)
+        self.qx4, self.sx4, _, _ = fb.fp8blk_quantize_mx4(self.x, fb.MXFP4)
+
+    def layer(self, **k):
+        """The layer functions: forward, few rows and backward over groups, then in 4 bits."""
+        return (fb.grouped_linear_forward(self.x, self.qw, self.sw, self.off, **k),
+                fb.grouped_linear_forward(self.x[:9], self.qw, self.sw, self.few, **k),
+                *fb.grouped_linear_backward(self.x, self.dy, self.qwT, self.swT, self.off, **k),
+                fb.mx4_linear_forward(self.x, self.q4, self.s4, fb.MXFP4, **k),
+                fb.mx4_linear_forward(self.x[:9], self.q4, self.s4, fb.MXFP4, **k),
+                fb.mx4_linear_wgrad(self.x, self.dy, fb.MXFP4, **k),
+                *fb.mx4_linear_backward(self.x, self.dy, self.q4T, self.s4T, fb.MXFP4, **k))
+
+
+@pytest.mark.parametrize("handle", ["0", "1", "current"])
+def test_handle_of_the_default_stream_keeps_its_order(handle):
+    """x and dy are written late on the default stream, and the results read on it at once: the calls wait for
+    the one and the reads for the calls."""
+    require_cuda()
+    c = Case()
+    x, dy = c.x.clone(), c.dy.clone()
+    want = c.layer()
+    torch.cuda.synchronize()
+    handle = torch.cuda.current_stream().cuda_stream if handle == "current" else int(handle)
+    c.x.zero_()
+    c.dy.zero_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(300_000_000)
+    c.x.copy_(x)
+    c.dy.copy_(dy)
+    got = [t.clone() for t in c.layer(stream=handle)]
+    torch.cuda.synchronize()
+    assert fb.fp8blk_get_device_error() == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
