@@ -133,6 +133,32 @@ def _bf16_2d(x):
     return x
 
 
+def _on_stream(stream, device, call):
+    """call() with `stream` current: what it allocates is that stream's memory, which no earlier work of
+    another stream still uses, and its results' memory is not given out again before the work that the
+    caller's current stream has for them is done."""
+    if not isinstance(stream, torch.cuda.Stream):
+        # Handles 0 and 1 are the legacy default stream (NULL and cudaStreamLegacy).  ExternalStream would take 0 for
+        # "no handle given" and make a stream of its own, and 1 for an identifier of its own streams.
+        handle = int(stream)
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = call()
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
+
+
+def _some_missing(mode, q_row, s_row, q_colT, s_colT) -> bool:
+    """Whether a quantiser of that mode has to make an output."""
+    return bool(mode & ROWWISE and (q_row is None or s_row is None) or
+                mode & COLWISE_T and (q_colT is None or s_colT is None))
+
+
 def fp8blk_quantize_act_1x128(x, mode=ROWWISE, q_row=None, s_row=None, q_colT=None, s_colT=None,
                               stream=None):
     """Activation quantisation in 1x128 groups.  Returns (q_row, s_row, q_colT, s_colT); unused are None.
@@ -420,6 +446,9 @@ def fp8blk_quantize_act_1x128_grouped(x, offsets, mode=ROWWISE, q_row=None, s_ro
     x = _bf16_2d(x)
     groups = _offsets(offsets)
     dev = _need_cuda(x, offsets, q_row, s_row, q_colT, s_colT)
+    if stream is not None and _some_missing(mode, q_row, s_row, q_colT, s_colT):
+        return _on_stream(stream, dev, lambda: fp8blk_quantize_act_1x128_grouped(x, offsets, mode, q_row, s_row, q_colT,
+                                                                                 s_colT))
     rows, cols = x.shape
     code_dtype = E5M2_DTYPE if mode & E5M2 else E4M3
     if mode & ROWWISE:
@@ -445,6 +474,9 @@ def fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, d=None, stream=None, out_
     out_dtype=torch.float32 or an fp32 d.  Rows of d outside every group are left as they were."""
     groups = _offsets(offsets)
     dev = _need_cuda(a, sa, b, sb, offsets, d)
+    if stream is not None and d is None:
+        return _on_stream(stream, dev,
+                          lambda: fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, out_dtype=out_dtype))
     if a.dim() != 2 or b.dim() != 2 or a.dtype not in (E4M3, E5M2_DTYPE) or b.dtype not in (E4M3, E5M2_DTYPE):
         raise ValueError("A and B must be 2-D float8_e4m3fn or float8_e5m2")
     m, k = a.shape
@@ -479,25 +511,6 @@ def fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, d=None, stream=None, out_
     _run(dev, lib.fp8blk_gemm_grouped, int(layout) | flags, groups, _ptr(offsets), m, n, k, _ptr(a), _ptr(sa), _ptr(b),
          _ptr(sb), _ptr(d), d.stride(-2) if layout == WGRAD else _pitch(d, n), _stream_handle(stream, dev))
     return d
-
-
-def _on_stream(stream, device, call):
-    """call() with `stream` current: what it allocates is that stream's memory, which no earlier work of
-    another stream still uses, and its results' memory is not given out again before the work that the
-    caller's current stream has for them is done."""
-    if not isinstance(stream, torch.cuda.Stream):
-        # Handles 0 and 1 are the legacy default stream (NULL and cudaStreamLegacy).  ExternalStream would take 0 for
-        # "no handle given" and make a stream of its own, and 1 for an identifier of its own streams.
-        handle = int(stream)
-        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=device)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    caller = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        out = call()
-    for t in out if isinstance(out, tuple) else (out,):
-        t.record_stream(caller)
-    return out
 
 
 def fp8blk_linear_grouped_workspace_bytes(groups: int, rows: int, k: int) -> int:
@@ -600,6 +613,9 @@ def fp8blk_quantize_mx4(x, fmt, mode=ROWWISE, tensor_scale=None, q_row=None, s_r
     if fmt not in MX4_BLOCK:
         raise ValueError("fmt must be MXFP4 or NVFP4")
     dev = _need_cuda(x, _tensor_scale(tensor_scale), q_row, s_row, q_colT, s_colT)
+    if stream is not None and _some_missing(mode, q_row, s_row, q_colT, s_colT):
+        return _on_stream(stream, dev,
+                          lambda: fp8blk_quantize_mx4(x, fmt, mode, tensor_scale, q_row, s_row, q_colT, s_colT))
     rows, cols = x.shape
     if mode & ROWWISE:
         q_row = _out(q_row, (rows, cols // 2), torch.uint8, dev)
@@ -623,6 +639,8 @@ def fp8blk_dequantize_mx4(q, s, fmt, tensor_scale=None, y=None, stream=None):
     if fmt not in MX4_BLOCK:
         raise ValueError("fmt must be MXFP4 or NVFP4")
     dev = _need_cuda(q, s, _tensor_scale(tensor_scale), y)
+    if stream is not None and y is None:
+        return _on_stream(stream, dev, lambda: fp8blk_dequantize_mx4(q, s, fmt, tensor_scale))
     rows, cols = _mx4_operand(q, s, fmt, "q")
     if y is None:
         y = _empty((rows, cols), torch.bfloat16, dev)
@@ -639,6 +657,9 @@ def fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa=None, tensor_sb=None, d=None, s
     if fmt not in MX4_BLOCK:
         raise ValueError("fmt must be MXFP4 or NVFP4")
     dev = _need_cuda(a, sa, b, sb, _tensor_scale(tensor_sa), _tensor_scale(tensor_sb), d)
+    if stream is not None and d is None:
+        return _on_stream(stream, dev,
+                          lambda: fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa, tensor_sb, out_dtype=out_dtype))
     m, k = _mx4_operand(a, sa, fmt, "A")
     n, kb = _mx4_operand(b, sb, fmt, "B")
     if k != kb:

@@ -63,3 +63,51 @@ def test_handle_of_the_default_stream_keeps_its_order(handle):
     assert fb.fp8blk_get_device_error() == 0
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+PRIMITIVES = {
+    "quantize_grouped": lambda c, **k: fb.fp8blk_quantize_act_1x128_grouped(c.x, c.off, fb.BOTH, **k),
+    "gemm_grouped": lambda c, **k: fb.fp8blk_gemm_grouped(fb.FWD, c.qx, c.sx, c.qw, c.sw, c.off, **k),
+    "quantize_mx4": lambda c, **k: fb.fp8blk_quantize_mx4(c.x, fb.MXFP4, fb.BOTH, **k),
+    "dequantize_mx4": lambda c, **k: fb.fp8blk_dequantize_mx4(c.q4, c.s4, fb.MXFP4, **k),
+    "gemm_mx4": lambda c, **k: fb.fp8blk_gemm_mx4(c.qx4, c.sx4, c.q4, c.s4, fb.MXFP4, **k),
+}
+
+
+def _bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+def _check_allocation(call):
+    """Blocks of every size, freed behind a long queue of writes of NaN on the current stream, are not handed to a
+    call on another stream."""
+    want = call()
+    want = want if isinstance(want, tuple) else (want,)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        blocks = [torch.empty(1 << b, dtype=torch.uint8, device="cuda") for b in range(9, 24) for _ in range(3)]
+        for _ in range(40):
+            for b in blocks:
+                b.fill_(255)
+        taken = [(b.data_ptr(), b.data_ptr() + b.numel()) for b in blocks]
+        del blocks, b
+        got = call(stream=stream)
+        got = got if isinstance(got, tuple) else (got,)
+        torch.cuda.synchronize()
+        assert fb.fp8blk_get_device_error() == 0
+        for g, w in zip(got, want):
+            if w is None:
+                assert g is None
+                continue
+            assert not any(lo <= g.data_ptr() < hi for lo, hi in taken)
+            assert g.shape == w.shape and g.dtype == w.dtype
+            assert torch.equal(_bits(g), _bits(w))
+        del got, g
+
+
+@pytest.mark.parametrize("name", PRIMITIVES)
+def test_primitives_allocate_from_the_named_stream(name):
+    require_cuda()
+    c = Case()
+    _check_allocation(lambda **k: PRIMITIVES[name](c, **k))

@@ -44,3 +44,65 @@ def test_handle_of_the_default_stream_is_that_stream(streams, handle, name):
 
     fb._on_stream(handle, CPU, call)
     assert seen == [name] and streams[-1].name == "caller"
+
+
+def _args():
+    """Tensors that pass the binding's checks, on the CPU."""
+    f8, u8, f32 = torch.float8_e4m3fn, torch.uint8, torch.float32
+    z = lambda *shape, t=torch.bfloat16: torch.zeros(shape, dtype=t)  # noqa: E731
+    return {"x": z(128, 128), "off": torch.zeros(2, dtype=torch.int32), "q": z(128, 128, t=f8), "s": z(1, 128, t=f32),
+            "sw": z(1, 1, t=f32), "q4": z(128, 64, t=u8), "s4": z(1, 1, 512, t=u8), "d": z(128, 128)}
+
+
+GROUPED_AND_MX4 = {
+    "quantize_grouped": lambda a, **k: fb.fp8blk_quantize_act_1x128_grouped(a["x"], a["off"], fb.BOTH, **k),
+    "quantize_grouped_some_given": lambda a, **k: fb.fp8blk_quantize_act_1x128_grouped(
+        a["x"], a["off"], fb.BOTH, q_row=a["q"], s_row=a["s"], **k),
+    "gemm_grouped": lambda a, **k: fb.fp8blk_gemm_grouped(fb.FWD, a["q"], a["s"], a["q"], a["sw"], a["off"], **k),
+    "linear_grouped": lambda a, **k: fb.fp8blk_linear_grouped(a["x"], a["q"], a["sw"], a["off"], **k),
+    "quantize_mx4": lambda a, **k: fb.fp8blk_quantize_mx4(a["x"], fb.MXFP4, fb.COLWISE_T, **k),
+    "dequantize_mx4": lambda a, **k: fb.fp8blk_dequantize_mx4(a["q4"], a["s4"], fb.MXFP4, **k),
+    "gemm_mx4": lambda a, **k: fb.fp8blk_gemm_mx4(a["q4"], a["s4"], a["q4"], a["s4"], fb.MXFP4, **k),
+    "linear_mx4": lambda a, **k: fb.fp8blk_linear_mx4(a["x"], a["q4"], a["s4"], fb.MXFP4, **k),
+}
+
+
+@pytest.fixture
+def made(streams, monkeypatch):
+    """(shape, name of the current stream) of every tensor that a call makes; the library is not called."""
+    seen = []
+    real = torch.empty, torch.empty_strided
+
+    def note(make):
+        def made_by(shape, *args, **kwargs):
+            seen.append((tuple(shape) if not isinstance(shape, int) else (shape,), streams[-1].name))
+            return make(shape, *args, **kwargs)
+        return made_by
+
+    monkeypatch.setattr(torch, "empty", note(real[0]))
+    monkeypatch.setattr(torch, "empty_strided", note(real[1]))
+    monkeypatch.setattr(fb, "_need_cuda", lambda *tensors: CPU)
+    monkeypatch.setattr(fb, "_run", lambda *args: None)
+    monkeypatch.setattr(fb, "_stream_handle", lambda stream, device=None: 0)
+    return seen
+
+
+@pytest.mark.parametrize("name", GROUPED_AND_MX4)
+def test_missing_outputs_come_from_the_named_stream(made, name):
+    """Memory of the caller's current stream may still be written by that stream's earlier work."""
+    GROUPED_AND_MX4[name](_args(), stream=0x7F00)
+    assert made and {where for _, where in made} == {0x7F00}
+    made.clear()
+    GROUPED_AND_MX4[name](_args())
+    assert made and {where for _, where in made} == {"caller"}
+
+
+def test_nothing_is_made_where_every_output_is_given(made):
+    a = _args()
+    for call in (lambda **k: fb.fp8blk_quantize_act_1x128_grouped(a["x"], a["off"], q_row=a["q"], s_row=a["s"], **k),
+                 lambda **k: fb.fp8blk_gemm_grouped(fb.FWD, a["q"], a["s"], a["q"], a["sw"], a["off"], d=a["d"], **k),
+                 lambda **k: fb.fp8blk_quantize_mx4(a["x"], fb.MXFP4, q_row=a["q4"], s_row=a["s4"], **k),
+                 lambda **k: fb.fp8blk_dequantize_mx4(a["q4"], a["s4"], fb.MXFP4, y=a["d"], **k),
+                 lambda **k: fb.fp8blk_gemm_mx4(a["q4"], a["s4"], a["q4"], a["s4"], fb.MXFP4, d=a["d"], **k)):
+        call(stream=0x7F00)
+    assert not made
