@@ -7,7 +7,11 @@ nvcc to build it) raises, and every call on a non-CUDA tensor raises.
 
 The functions carry the C-ABI's names (include/fp8blk.h).  Output tensors
 may be passed in (they must be contiguous CUDA tensors of the right dtype
-and shape); missing ones are allocated with torch.empty.
+and shape); missing ones are allocated with torch.empty, on the stream of
+the call: the current one, or the one passed as ``stream`` (a
+torch.cuda.Stream or a cudaStream_t handle).  A stream that is passed in is
+ordered against no other stream by the call: the caller orders the inputs
+before it and keeps them until it is done.
 
 Layouts (row-major, dimensions multiples of 128):
   fp8blk_quantize_act_1x128(x[R,C], mode)
@@ -133,6 +137,15 @@ def _bf16_2d(x):
     return x
 
 
+def _record(out, stream) -> None:
+    """Marks a result (a tensor, None, or a tuple or list of results) as used by `stream`."""
+    if isinstance(out, (tuple, list)):
+        for t in out:
+            _record(t, stream)
+    elif out is not None:
+        out.record_stream(stream)
+
+
 def _on_stream(stream, device, call):
     """call() with `stream` current: what it allocates is that stream's memory, which no earlier work of
     another stream still uses, and its results' memory is not given out again before the work that the
@@ -147,9 +160,7 @@ def _on_stream(stream, device, call):
     caller = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
         out = call()
-    for t in out if isinstance(out, tuple) else (out,):
-        if t is not None:
-            t.record_stream(caller)
+    _record(out, caller)
     return out
 
 
@@ -165,8 +176,9 @@ def fp8blk_quantize_act_1x128(x, mode=ROWWISE, q_row=None, s_row=None, q_colT=No
     ``mode`` may include E5M2 (codes as torch.float8_e5m2, for gradients)."""
     x = _bf16_2d(x)
     dev = _need_cuda(x)
+    if stream is not None and _some_missing(mode, q_row, s_row, q_colT, s_colT):
+        return _on_stream(stream, dev, lambda: fp8blk_quantize_act_1x128(x, mode, q_row, s_row, q_colT, s_colT))
     rows, cols = x.shape
-    dev = x.device
     code_dtype = E5M2_DTYPE if mode & E5M2 else E4M3
     if mode & ROWWISE:
         q_row = _out(q_row, (rows, cols), code_dtype, dev)
@@ -187,6 +199,8 @@ def fp8blk_quantize_weight_128x128(w, q=None, s=None, stream=None):
     """Weight quantisation in 128x128 blocks.  Returns (q[N,K], s[N/128,K/128])."""
     w = _bf16_2d(w)
     dev = _need_cuda(w)
+    if stream is not None and any(t is None for t in (q, s)):
+        return _on_stream(stream, dev, lambda: fp8blk_quantize_weight_128x128(w, q, s))
     n, k = w.shape
     q = _out(q, (n, k), E4M3, w.device)
     s = _out(s, (n // 128, k // 128), torch.float32, w.device)
@@ -198,6 +212,8 @@ def fp8blk_quantize_weight_128x128_t(w, qT=None, sT=None, stream=None):
     """The same blocks written transposed.  Returns (qT[K,N], sT[K/128,N/128])."""
     w = _bf16_2d(w)
     dev = _need_cuda(w)
+    if stream is not None and any(t is None for t in (qT, sT)):
+        return _on_stream(stream, dev, lambda: fp8blk_quantize_weight_128x128_t(w, qT, sT))
     n, k = w.shape
     qT = _out(qT, (k, n), E4M3, w.device)
     sT = _out(sT, (k // 128, n // 128), torch.float32, w.device)
@@ -210,6 +226,8 @@ def fp8blk_quantize_weight_128x128_both(w, q=None, s=None, qT=None, sT=None, str
     """Both block layouts from one read of w.  Returns (q[N,K], s[N/128,K/128], qT[K,N], sT[K/128,N/128])."""
     w = _bf16_2d(w)
     dev = _need_cuda(w)
+    if stream is not None and any(t is None for t in (q, s, qT, sT)):
+        return _on_stream(stream, dev, lambda: fp8blk_quantize_weight_128x128_both(w, q, s, qT, sT))
     n, k = w.shape
     q = _out(q, (n, k), E4M3, w.device)
     s = _out(s, (n // 128, k // 128), torch.float32, w.device)
@@ -237,6 +255,8 @@ def fp8blk_gemm(layout, a, sa, b, sb, d=None, stream=None, out_dtype=torch.bfloa
     fp32 partials are summed in split order; workspace: a float32 CUDA tensor of at least
     fp8blk_gemm_splitk_workspace_bytes(...) bytes (allocated here when None)."""
     dev = _need_cuda(a, sa, b, sb, d)
+    if stream is not None and (d is None or (workspace is None and splits != 1)):
+        return _on_stream(stream, dev, lambda: fp8blk_gemm(layout, a, sa, b, sb, d, None, out_dtype, splits, workspace))
     m, k = a.shape
     n = b.shape[0]
     if b.shape[1] != k:
@@ -286,6 +306,8 @@ def fp8blk_gemm_splitk(layout, a, sa, b, sb, splits, d=None, workspace=None, str
 def fp8blk_round_f32_to_bf16(x, y=None, stream=None):
     """y = bf16(x) (round to nearest even), elementwise; x a contiguous float32 CUDA tensor."""
     dev = _need_cuda(x, y)
+    if stream is not None and y is None:
+        return _on_stream(stream, dev, lambda: fp8blk_round_f32_to_bf16(x))
     if x.dtype != torch.float32 or not x.is_contiguous():
         raise ValueError("x must be a contiguous float32 tensor")
     y = _out(y, tuple(x.shape), torch.bfloat16, x.device)
@@ -307,6 +329,8 @@ def fp8blk_quantize_weights_128x128_both(weights, outs=None, stream=None):
     weights = [_bf16_2d(w) for w in weights]
     flat = [t for w, o in zip(weights, outs) for t in (w, *(o or ()))]
     dev = _need_cuda(*flat)
+    if stream is not None and any(o is None or any(t is None for t in o) for o in outs):
+        return _on_stream(stream, dev, lambda: fp8blk_quantize_weights_128x128_both(weights, outs))
     descs = (WeightDesc * len(weights))()
     result = []
     for i, (w, o) in enumerate(zip(weights, outs)):
@@ -331,6 +355,8 @@ def fp8blk_amax_ema(x, amax, scale=None, workspace=None, stream=None):
     EMA and write the tensor's scale.  Returns (amax, scale)."""
     x = _bf16_2d(x)
     dev = _need_cuda(x, amax, scale, workspace)
+    if stream is not None and (scale is None or workspace is None):
+        return _on_stream(stream, dev, lambda: fp8blk_amax_ema(x, amax, scale, workspace))
     rows, cols = x.shape
     if amax.dtype != torch.float32 or amax.numel() != 1:
         raise ValueError("amax must be a float32 tensor with one element")
@@ -367,6 +393,8 @@ def fp8blk_quantize_tensor(x, scale, q=None, stream=None):
     """The whole tensor with its one scale (device float32 [1]).  Returns q [rows, cols] E4M3."""
     x = _bf16_2d(x)
     dev = _need_cuda(x, scale, q)
+    if stream is not None and q is None:
+        return _on_stream(stream, dev, lambda: fp8blk_quantize_tensor(x, scale))
     rows, cols = x.shape
     q = _out(q, (rows, cols), E4M3, x.device)
     _run(dev, lib.fp8blk_quantize_tensor, _ptr(x), rows, cols, x.stride(0), _ptr(scale), _ptr(q), _stream_handle(stream, dev))
@@ -376,6 +404,8 @@ def fp8blk_quantize_tensor(x, scale, q=None, stream=None):
 def fp8blk_gemm_tensor_scaled(a, sa, b, sb, d=None, stream=None):
     """D[M,N] = bf16(sa * sb * A . B^T) with one scale per E4M3 operand (device float32 [1] each)."""
     dev = _need_cuda(a, sa, b, sb, d)
+    if stream is not None and d is None:
+        return _on_stream(stream, dev, lambda: fp8blk_gemm_tensor_scaled(a, sa, b, sb))
     m, k = a.shape
     n = b.shape[0]
     if b.shape[1] != k or a.dtype != E4M3 or b.dtype != E4M3:
@@ -390,11 +420,13 @@ def fp8blk_gemm_tensor_scaled(a, sa, b, sb, d=None, stream=None):
 def fp8_linear_delayed_forward(x, w, x_amax, w_amax, stream=None):
     """Y = X . W^T with per-tensor delayed scaling: both amax buffers updated by the EMA, both
     tensors quantised with their one scale, one GEMM.  Returns Y (bf16)."""
-    _, sx = fp8blk_amax_ema(x, x_amax, stream=stream)
-    _, sw = fp8blk_amax_ema(w, w_amax, stream=stream)
-    qx = fp8blk_quantize_tensor(x, sx, stream=stream)
-    qw = fp8blk_quantize_tensor(w, sw, stream=stream)
-    return fp8blk_gemm_tensor_scaled(qx, sx, qw, sw, stream=stream)
+    if stream is not None:
+        return _on_stream(stream, _need_cuda(x, w), lambda: fp8_linear_delayed_forward(x, w, x_amax, w_amax))
+    _, sx = fp8blk_amax_ema(x, x_amax)
+    _, sw = fp8blk_amax_ema(w, w_amax)
+    qx = fp8blk_quantize_tensor(x, sx)
+    qw = fp8blk_quantize_tensor(w, sw)
+    return fp8blk_gemm_tensor_scaled(qx, sx, qw, sw)
 
 
 def fp8blk_get_device_error(stream=None) -> int:
@@ -408,18 +440,22 @@ def fp8blk_version() -> int:
 
 def linear_forward(x, w, stream=None):
     """Y = X . W^T through the FP8 blockwise path: quantise X (1x128) and W (128x128), then GEMM."""
-    qx, sx, _, _ = fp8blk_quantize_act_1x128(x, ROWWISE, stream=stream)
-    qw, sw = fp8blk_quantize_weight_128x128(w, stream=stream)
-    return fp8blk_gemm(FWD, qx, sx, qw, sw, stream=stream)
+    if stream is not None:
+        return _on_stream(stream, _need_cuda(x, w), lambda: linear_forward(x, w))
+    qx, sx, _, _ = fp8blk_quantize_act_1x128(x, ROWWISE)
+    qw, sw = fp8blk_quantize_weight_128x128(w)
+    return fp8blk_gemm(FWD, qx, sx, qw, sw)
 
 
 def linear_backward(x, w, dy, stream=None):
     """(dX, dW) of Y = X . W^T: dX = dY . W (dgrad), dW = dY^T . X (wgrad), both FP8 blockwise."""
-    qdy, sdy, qdyT, sdyT = fp8blk_quantize_act_1x128(dy, BOTH, stream=stream)
-    qwT, swT = fp8blk_quantize_weight_128x128_t(w, stream=stream)
-    _, _, qxT, sxT = fp8blk_quantize_act_1x128(x, COLWISE_T, stream=stream)
-    dx = fp8blk_gemm(DGRAD, qdy, sdy, qwT, swT, stream=stream)
-    dw = fp8blk_gemm(WGRAD, qdyT, sdyT, qxT, sxT, stream=stream)
+    if stream is not None:
+        return _on_stream(stream, _need_cuda(x, w, dy), lambda: linear_backward(x, w, dy))
+    qdy, sdy, qdyT, sdyT = fp8blk_quantize_act_1x128(dy, BOTH)
+    qwT, swT = fp8blk_quantize_weight_128x128_t(w)
+    _, _, qxT, sxT = fp8blk_quantize_act_1x128(x, COLWISE_T)
+    dx = fp8blk_gemm(DGRAD, qdy, sdy, qwT, swT)
+    dw = fp8blk_gemm(WGRAD, qdyT, sdyT, qxT, sxT)
     return dx, dw
 
 

@@ -24,6 +24,7 @@ class Case:
         self.off = torch.tensor([0, 100, T], dtype=torch.int32, device="cuda")
         self.few = self.off.clamp(max=9)
         self.one = torch.tensor([0.01], device="cuda")
+        self.amax = [self.one.clone() for _ in range(8)]         # one for every call that updates it
         w2 = torch.cat([self.w, self.w])
         self.qw, self.sw, self.qwT, self.swT = fb.fp8blk_quantize_weight_128x128_both(w2)
         self.q4, self.s4, self.q4T, self.s4T = fb.fp8blk_quantize_mx4(self.w, fb.MXFP4, fb.BOTH)
@@ -73,6 +74,22 @@ PRIMITIVES = {
     "gemm_mx4": lambda c, **k: fb.fp8blk_gemm_mx4(c.qx4, c.sx4, c.q4, c.s4, fb.MXFP4, **k),
 }
 
+BLOCKWISE = {
+    "quantize_act": lambda c, **k: fb.fp8blk_quantize_act_1x128(c.x, fb.BOTH, **k),
+    "quantize_weight": lambda c, **k: fb.fp8blk_quantize_weight_128x128(c.w, **k),
+    "quantize_weight_t": lambda c, **k: fb.fp8blk_quantize_weight_128x128_t(c.w, **k),
+    "quantize_weight_both": lambda c, **k: fb.fp8blk_quantize_weight_128x128_both(c.w, **k),
+    "quantize_weights": lambda c, **k: tuple(t for o in fb.fp8blk_quantize_weights_128x128_both([c.w, c.w], **k) for t in o),
+    "gemm": lambda c, **k: fb.fp8blk_gemm(fb.FWD, c.qx, c.sx, c.q1, c.s1, **k),
+    "gemm_splitk": lambda c, **k: fb.fp8blk_gemm_splitk(fb.FWD, c.qx, c.sx, c.q1, c.s1, 2, **k),
+    "amax_ema": lambda c, **k: fb.fp8blk_amax_ema(c.x, c.amax.pop(), **k)[1],
+    "quantize_tensor": lambda c, **k: fb.fp8blk_quantize_tensor(c.x, c.one, **k),
+    "gemm_tensor_scaled": lambda c, **k: fb.fp8blk_gemm_tensor_scaled(c.qx, c.one, c.q1, c.one, **k),
+    "linear_forward": lambda c, **k: fb.linear_forward(c.x, c.w, **k),
+    "linear_backward": lambda c, **k: fb.linear_backward(c.x, c.w, c.dy, **k),
+    "linear_delayed": lambda c, **k: fb.fp8_linear_delayed_forward(c.x, c.w, c.amax.pop(), c.amax.pop(), **k),
+}
+
 
 def _bits(t):
     return t.contiguous().view(torch.uint8)
@@ -111,3 +128,11 @@ def test_primitives_allocate_from_the_named_stream(name):
     require_cuda()
     c = Case()
     _check_allocation(lambda **k: PRIMITIVES[name](c, **k))
+
+
+@pytest.mark.parametrize("name", BLOCKWISE)
+def test_blockwise_calls_allocate_from_the_named_stream(name):
+    require_cuda()
+    c = Case()
+    torch.cuda.synchronize()
+    _check_allocation(lambda **k: BLOCKWISE[name](c, **k))

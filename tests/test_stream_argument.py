@@ -51,7 +51,7 @@ def _args():
     f8, u8, f32 = torch.float8_e4m3fn, torch.uint8, torch.float32
     z = lambda *shape, t=torch.bfloat16: torch.zeros(shape, dtype=t)  # noqa: E731
     return {"x": z(128, 128), "off": torch.zeros(2, dtype=torch.int32), "q": z(128, 128, t=f8), "s": z(1, 128, t=f32),
-            "sw": z(1, 1, t=f32), "q4": z(128, 64, t=u8), "s4": z(1, 1, 512, t=u8), "d": z(128, 128)}
+            "sw": z(1, 1, t=f32), "q4": z(128, 64, t=u8), "s4": z(1, 1, 512, t=u8), "d": z(128, 128), "one": torch.ones(1)}
 
 
 GROUPED_AND_MX4 = {
@@ -84,16 +84,38 @@ def made(streams, monkeypatch):
     monkeypatch.setattr(fb, "_need_cuda", lambda *tensors: CPU)
     monkeypatch.setattr(fb, "_run", lambda *args: None)
     monkeypatch.setattr(fb, "_stream_handle", lambda stream, device=None: 0)
+    monkeypatch.setattr(fb, "fp8blk_gemm_splitk_workspace_bytes", lambda *args: 128 * 128 * 4)
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
     return seen
 
 
-@pytest.mark.parametrize("name", GROUPED_AND_MX4)
+BLOCKWISE = {
+    "quantize_act": lambda a, **k: fb.fp8blk_quantize_act_1x128(a["x"], fb.BOTH, **k),
+    "quantize_act_some_given": lambda a, **k: fb.fp8blk_quantize_act_1x128(a["x"], q_row=a["q"], **k),
+    "quantize_weight": lambda a, **k: fb.fp8blk_quantize_weight_128x128(a["x"], q=a["q"], **k),
+    "quantize_weight_t": lambda a, **k: fb.fp8blk_quantize_weight_128x128_t(a["x"], **k),
+    "quantize_weight_both": lambda a, **k: fb.fp8blk_quantize_weight_128x128_both(a["x"], **k),
+    "quantize_weights": lambda a, **k: fb.fp8blk_quantize_weights_128x128_both([a["x"], a["x"]], **k),
+    "gemm": lambda a, **k: fb.fp8blk_gemm(fb.FWD, a["q"], a["s"], a["q"], a["sw"], **k),
+    "gemm_splitk_workspace": lambda a, **k: fb.fp8blk_gemm_splitk(fb.FWD, a["q"], a["s"], a["q"], a["sw"], 2, d=a["d"], **k),
+    "round": lambda a, **k: fb.fp8blk_round_f32_to_bf16(a["s"], **k),
+    "amax_ema": lambda a, **k: fb.fp8blk_amax_ema(a["x"], a["one"], scale=a["one"], **k),
+    "quantize_tensor": lambda a, **k: fb.fp8blk_quantize_tensor(a["x"], a["one"], **k),
+    "gemm_tensor_scaled": lambda a, **k: fb.fp8blk_gemm_tensor_scaled(a["q"], a["one"], a["q"], a["one"], **k),
+    "linear_forward": lambda a, **k: fb.linear_forward(a["x"], a["x"], **k),
+    "linear_backward": lambda a, **k: fb.linear_backward(a["x"], a["x"], a["x"], **k),
+    "linear_delayed": lambda a, **k: fb.fp8_linear_delayed_forward(a["x"], a["x"], a["one"], a["one"], **k),
+}
+EVERY = {**GROUPED_AND_MX4, **BLOCKWISE}
+
+
+@pytest.mark.parametrize("name", EVERY)
 def test_missing_outputs_come_from_the_named_stream(made, name):
     """Memory of the caller's current stream may still be written by that stream's earlier work."""
-    GROUPED_AND_MX4[name](_args(), stream=0x7F00)
+    EVERY[name](_args(), stream=0x7F00)
     assert made and {where for _, where in made} == {0x7F00}
     made.clear()
-    GROUPED_AND_MX4[name](_args())
+    EVERY[name](_args())
     assert made and {where for _, where in made} == {"caller"}
 
 
