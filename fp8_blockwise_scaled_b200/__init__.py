@@ -117,8 +117,8 @@ def _empty(shape, dtype, device):
 def _out(t, shape, dtype, device):
     if t is None:
         return _empty(shape, dtype, device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"output must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"output must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 

@@ -128,3 +128,11 @@ def test_nothing_is_made_where_every_output_is_given(made):
                  lambda **k: fb.fp8blk_gemm_mx4(a["q4"], a["s4"], a["q4"], a["s4"], fb.MXFP4, d=a["d"], **k)):
         call(stream=0x7F00)
     assert not made
+
+
+def test_outputs_of_another_device_are_refused():
+    """A host pointer, or another GPU's, would reach the kernel."""
+    t = torch.zeros(4, 8)
+    assert fb._out(t, (4, 8), torch.float32, CPU) is t
+    with pytest.raises(ValueError, match="on cuda:0"):
+        fb._out(t, (4, 8), torch.float32, torch.device("cuda", 0))
