@@ -85,12 +85,26 @@ __device__ __forceinline__ uint32_t nvfp4_scale(float amax, float g, float rg) {
   return cvt_e4m3(t) & 0x7Fu;
 }
 
-// What the values of an NVFP4 block with that scale byte are divided by.
+// What the values of an NVFP4 block with that scale byte are divided by.  nr: +0 for
+// a divisor of zero, else negative (finish_codes), also for one that is no number.
 __device__ __forceinline__ QScale nvfp4_divisor(uint32_t byte, float g) {
   QScale q;
   q.s = e4m3_value(byte) * g;
-  q.nr = q.s > 0.0f ? -__frcp_rn(q.s) : 0.0f;
+  q.nr = q.s > 0.0f ? -__frcp_rn(q.s) : (q.s == 0.0f ? 0.0f : -1.0f);
   return q;
+}
+
+// Codes of NVFP4 values: the negated quotient's signs flipped back, and zeros of no
+// sign where the block's divisor is zero (there the quotient's sign follows x).  nr
+// is negative but for that divisor, so its sign bit, spread over the word, is the
+// mask (16384 x 8960 in both directions: 1.6% of the time; with a comparison and a
+// select 5%).
+template <bool kNv>
+__device__ __forceinline__ uint32_t finish_codes(uint32_t codes, float nr) {
+  if constexpr (!kNv) return codes;
+  uint32_t keep;
+  asm("prmt.b32 %0, %1, 0, 0xBBBB;" : "=r"(keep) : "r"(__float_as_uint(nr)));
+  return (codes ^ 0x88888888u) & keep;
 }
 
 template <bool kNv>

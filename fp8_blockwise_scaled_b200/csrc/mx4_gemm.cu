@@ -661,7 +661,7 @@ __device__ __forceinline__ uint32_t quant_block(const uint4* w, int n, float g, 
       v[j] = r.x;
       v[j + 1] = r.y;
     }
-    codes[i] = cvt8_e2m1(v) ^ (kNv ? 0x88888888u : 0u);
+    codes[i] = finish_codes<kNv>(cvt8_e2m1(v), q.nr);
   }
   return byte;
 }

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
           hi8[c] = w.y;
         }
         // Neighbouring lanes exchange halves: the even lane stores 16 columns of row 2p, the odd one of row 2p + 1.
-        const uint32_t lo_c = cvt8_e2m1(lo8) ^ (kNv ? 0x88888888u : 0u), hi_c = cvt8_e2m1(hi8) ^ (kNv ? 0x88888888u : 0u);
+        const uint32_t lo_c = finish_codes<kNv>(cvt8_e2m1(lo8), nr2.x), hi_c = finish_codes<kNv>(cvt8_e2m1(hi8), nr2.y);
         const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? lo_c : hi_c, 1);
         const int64_t row = row0 + r0 + 2 * p + (lane & 1);
         const int64_t col = col0 + c0 - 8 * (lane & 1);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         *reinterpret_cast<uint32_t*>(ctrl->codes_t + (c0 + c) * 64 + (((warp >> 1) ^ (bj & 3)) << 4) +
-                                     ((lane >> 3) << 2)) = line[c] ^ (kNv ? 0x88888888u : 0u);
+                                     ((lane >> 3) << 2)) = finish_codes<kNv>(line[c], cn[c]);
     }
     __syncthreads();                       // the staged scales and lines are complete
     if constexpr (kRow) {

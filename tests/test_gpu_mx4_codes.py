@@ -1,0 +1,72 @@
+"""The 4-bit quantiser's codes with their signs, and what it makes of values that are not finite."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_blockwise_scaled_b200 as fb
+import workloads
+from tests import mx4_reference as ref
+from tests.gpu_helpers import require_cuda, to_dev
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = {"mxfp4": fb.MXFP4, "nvfp4": fb.NVFP4}
+
+
+def _scalar(g):
+    return None if g is None else torch.tensor([g], dtype=torch.float32, device="cuda")
+
+
+def _x(rows, cols, seed):
+    """Both signs of zero, zero blocks, and blocks of both signs that are too small for any scale but zero."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((rows, cols)).astype(np.float32)
+    x[rng.random((rows, cols)) < 0.1] = 0.0
+    x[rng.random((rows, cols)) < 0.1] = -0.0
+    tiny = rng.random((-(-rows // 32), cols // 16)) < 0.3
+    tiny = np.repeat(np.repeat(tiny, 32, 0), 16, 1)[:rows]
+    x[tiny] *= np.float32(1e-9)
+    empty = np.repeat(np.repeat(rng.random((-(-rows // 32), cols // 16)) < 0.2, 32, 0), 16, 1)[:rows]
+    x[empty] = np.where(rng.random(x[empty].shape) < 0.5, 0.0, -0.0)
+    return workloads.f32_to_bf16(x)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 32), (31, 160), (300, 416)])
+@pytest.mark.parametrize("fmt,g", [("mxfp4", None), ("nvfp4", None), ("nvfp4", 0.0071)])
+def test_codes_with_their_signs(rows, cols, fmt, g):
+    """A block whose NVFP4 scale is zero has the codes 0, whatever its signs; elsewhere zeros keep theirs."""
+    require_cuda()
+    bits = _x(rows, cols, rows + cols)
+    x = workloads.bf16_to_f32(bits).astype(np.float64)
+    q, s, qT, sT = fb.fp8blk_quantize_mx4(to_dev(bits), FORMATS[fmt], fb.BOTH, _scalar(g))
+    q1, _, _, _ = fb.fp8blk_quantize_mx4(to_dev(bits), FORMATS[fmt], fb.ROWWISE, _scalar(g))
+    assert fb.fp8blk_get_device_error() == 0
+    codes, byte = ref.quantize(x, fmt, g or 1.0)
+    codesT, byteT = ref.quantize(np.ascontiguousarray(ref.pad_rows(x).T), fmt, g or 1.0)
+    if fmt == "nvfp4" and rows > 1:
+        assert (byte == 0).any() and (byteT == 0).any()
+    assert np.array_equal(s.cpu().numpy(), ref.tile(byte)) and np.array_equal(sT.cpu().numpy(), ref.tile(byteT))
+    assert np.array_equal(ref.unpack(q.cpu().numpy()), codes)
+    assert np.array_equal(ref.unpack(q1.cpu().numpy()), codes)
+    assert np.array_equal(ref.unpack(qT.cpu().numpy()), codesT)
+
+
+def test_zeros_come_back_without_a_sign():
+    require_cuda()
+    x = torch.zeros((40, 96), dtype=torch.bfloat16, device="cuda")
+    for fmt in FORMATS.values():
+        q, s, qT, sT = fb.fp8blk_quantize_mx4(x, fmt, fb.BOTH)
+        for a, b in ((q, s), (qT, sT)):
+            assert not bool(a.any()) and not bool(fb.fp8blk_dequantize_mx4(a, b, fmt).view(torch.int16).any())
+
+
+def test_few_rows_quantised_on_the_way_have_the_same_codes():
+    """Rows of zero blocks and tiny values of both signs: bit for bit the product of the quantiser's codes."""
+    require_cuda()
+    x, w = to_dev(_x(16, 416, 1)), to_dev(_x(72, 416, 2))
+    qw, sw, _, _ = fb.fp8blk_quantize_mx4(w, fb.NVFP4, tensor_scale=_scalar(0.0071))
+    qx, sx, _, _ = fb.fp8blk_quantize_mx4(x, fb.NVFP4, tensor_scale=_scalar(0.0071))
+    want = fb.fp8blk_gemm_mx4(qx, sx, qw, sw, fb.NVFP4, _scalar(0.0071), _scalar(0.0071), out_dtype=torch.float32)
+    got = fb.fp8blk_linear_mx4(x, qw, sw, fb.NVFP4, _scalar(0.0071), _scalar(0.0071), out_dtype=torch.float32)
+    assert fb.fp8blk_get_device_error() == 0
+    assert torch.equal(got.view(torch.int32), want.view(torch.int32))
