@@ -67,9 +67,9 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return f;
 }
 
-// An E8M0 byte's value, 2^(byte - 127) (byte 0: the subnormal 2^-127).
+// An E8M0 byte's value, 2^(byte - 127) (byte 0: the subnormal 2^-127; 255: NaN).
 __device__ __forceinline__ float e8m0_value(uint32_t byte) {
-  return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
 }
 
 // Scale byte of a block of maximum amax, and what its values are divided by.  g

@@ -351,7 +351,7 @@ int fp8blk_gemm_splitk_count(int layout, int64_t M, int64_t N, int64_t K);
  * 4-bit microscaled formats.  Codes are E2M1 (+-0, 0.5, 1, 1.5, 2, 3, 4, 6), two
  * to a byte, the lower index in the low nibble; blocks of consecutive values
  * along the contraction share a one-byte scale:
- *   FP8BLK_MXFP4  32 values, E8M0 (2^(byte - 127)); the OCP Microscaling rule
+ *   FP8BLK_MXFP4  32 values, E8M0 (2^(byte - 127), 255 is NaN); the OCP Microscaling rule
  *                   scale = 2^clamp(floor(log2 amax) - 2, -127, 127),
  *                   q = E2M1_round_nearest_even(clamp(x / scale, -6, 6))
  *   FP8BLK_NVFP4  16 values, E4M3, below one fp32 scale g for the tensor

@@ -70,3 +70,27 @@ def test_few_rows_quantised_on_the_way_have_the_same_codes():
     got = fb.fp8blk_linear_mx4(x, qw, sw, fb.NVFP4, _scalar(0.0071), _scalar(0.0071), out_dtype=torch.float32)
     assert fb.fp8blk_get_device_error() == 0
     assert torch.equal(got.view(torch.int32), want.view(torch.int32))
+
+
+def _dev8(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def test_e8m0_byte_255_is_nan_in_the_values_and_in_the_product():
+    """The format's NaN, whatever the codes below it; every other byte is its power of two."""
+    require_cuda()
+    codes = np.tile(np.arange(16, dtype=np.uint8), (256, 2))
+    byte = np.arange(256, dtype=np.uint8)[:, None]
+    y = fb.fp8blk_dequantize_mx4(_dev8(ref.pack(codes)), _dev8(ref.tile(byte)), fb.MXFP4).float().cpu().numpy()
+    assert np.isnan(y[255]).all()
+    with np.errstate(over="ignore"):
+        want = ref.values(codes[:255], byte[:255], "mxfp4").astype(np.float32)
+    assert np.array_equal(y[:255], torch.from_numpy(want).to(torch.bfloat16).float().numpy())
+    for m in (5, 200):
+        ones, scales = np.full((m, 64), 2, np.uint8), np.full((m, 2), 127, np.uint8)
+        scales[3, 1] = 255
+        a = _dev8(ref.pack(ones)), _dev8(ref.tile(scales))
+        b = _dev8(ref.pack(ones[:2])), _dev8(ref.tile(np.full((2, 2), 127, np.uint8)))
+        d = fb.fp8blk_gemm_mx4(*a, *b, fb.MXFP4, out_dtype=torch.float32).cpu().numpy()
+        assert np.isnan(d[3]).all() and (np.delete(d, 3, 0) == 64.0).all()
+    assert fb.fp8blk_get_device_error() == 0
