@@ -114,11 +114,27 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float g, float rg, Q
     q = nvfp4_divisor(byte, g);
     return byte;
   } else {
+    // amax is the largest bit pattern of the block without signs, so a NaN or an
+    // infinity in the block gives 253, which no finite amax does (finish_scales).
     const uint32_t byte = max(static_cast<int>(__float_as_uint(amax) >> 23) - 2, 0);
     q.s = 0.0f;
     q.nr = __uint_as_float((254u - byte) << 23);      // 1 / scale, exactly
     return byte;
   }
+}
+
+// Four scale bytes as they are stored: an MXFP4 block that holds a NaN or an infinity
+// (byte 253) gets 255, the format's NaN.  Done on the staged bytes, four at a time,
+// not where every thread of a block computes its scale (16384 x 8960, both
+// directions: 4% more time).
+template <bool kNv>
+__device__ __forceinline__ uint32_t finish_scales(uint32_t bytes) {
+  if constexpr (kNv) return bytes;
+  return bytes | ((((bytes & 0x7F7F7F7Fu) + 0x03030303u) & bytes & 0x80808080u) >> 6);
+}
+template <bool kNv>
+__device__ __forceinline__ uint4 finish_scales(uint4 v) {
+  return make_uint4(finish_scales<kNv>(v.x), finish_scales<kNv>(v.y), finish_scales<kNv>(v.z), finish_scales<kNv>(v.w));
 }
 
 // A pair of values by their blocks' scales: -RN(x / d) (NVFP4, whose code signs

@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kMxThreads, 2)
             static_cast<uint16_t>(b0 | (b1 << 8));
       } else {
         scales[(part >> 2) * kMx4AtomBytes + row * 16 + (part & 3)] =
-            static_cast<uint8_t>(quant_block<kNv>(w, 4, g, rg, c));
+            static_cast<uint8_t>(finish_scales<kNv>(quant_block<kNv>(w, 4, g, rg, c)));
       }
       *reinterpret_cast<uint4*>(codes + row * 128 + ((part ^ (row & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
       fence_proxy_async_shared();        // the writes above, then the tensor cores' reads

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
       const int64_t ka = static_cast<int64_t>(tc) * kAtoms + i;
       if (i < kAtoms && ka < atoms_k)
         *reinterpret_cast<uint4*>(a.s_row + (tr * atoms_k + ka) * kMx4AtomBytes + lane * 16) =
-            *reinterpret_cast<const uint4*>(ctrl->atoms + i * kMx4AtomBytes + lane * 16);
+            finish_scales<kNv>(*reinterpret_cast<const uint4*>(ctrl->atoms + i * kMx4AtomBytes + lane * 16));
     }
     if constexpr (kColT) {
       const int64_t padded = (a.rows + 31) / 32 * 32;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_quant_kernel(const __grid_con
       const int64_t ka = static_cast<int64_t>(tr) * kAtoms + i;
       if (i >= 0 && i < kAtoms && ka < atoms_k)
         *reinterpret_cast<uint4*>(a.s_t + (tc * atoms_k + ka) * kMx4AtomBytes + lane * 16) =
-            *reinterpret_cast<const uint4*>(ctrl->atoms_t + i * kMx4AtomBytes + lane * 16);
+            finish_scales<kNv>(*reinterpret_cast<const uint4*>(ctrl->atoms_t + i * kMx4AtomBytes + lane * 16));
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int k = t + kThreads * j, col = k >> 2, m = k & 3;

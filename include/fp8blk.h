@@ -29,7 +29,8 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream).  Work is enqueued asynchronously; argument errors are returned
  *    before anything is enqueued; a launch failure returns FP8BLK_ERR_LAUNCH.
- *  - Inputs must be finite; NaN or Inf in an input gives unspecified codes.
+ *  - Inputs must be finite; NaN or Inf in an input gives unspecified codes (in
+ *    the 4-bit formats below a scale that is NaN).
  *  - The quantisers are exact: codes and scales equal, bit for bit,
  *        s = max(fl32(amax / 448), fl32(1e-12))
  *        q = E4M3_round_nearest_even(clamp(fl32(x / s), -448, 448))
@@ -361,6 +362,9 @@ int fp8blk_gemm_splitk_count(int layout, int64_t M, int64_t N, int64_t K);
  *                   d = fl32(sf * g),
  *                   q = E2M1_round_nearest_even(clamp(fl32(x / d), -6, 6)), zeros where sf is 0
  *                 (|x| / g below 2^100 and g at least 1e-12, else unspecified codes).
+ * A block with a NaN or an infinity in it gets the format's NaN as its scale (E8M0
+ * 255, E4M3 0x7F) and unspecified codes: its values, and every sum of a product
+ * that it enters, are NaN.
  *
  * Scales are laid out as the tensor cores take them, for a [R][K] operand as
  *   [ceil(R / 128)][ceil(K / (4 * block))][512 bytes],

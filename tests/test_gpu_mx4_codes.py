@@ -94,3 +94,48 @@ def test_e8m0_byte_255_is_nan_in_the_values_and_in_the_product():
         d = fb.fp8blk_gemm_mx4(*a, *b, fb.MXFP4, out_dtype=torch.float32).cpu().numpy()
         assert np.isnan(d[3]).all() and (np.delete(d, 3, 0) == 64.0).all()
     assert fb.fp8blk_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("m", [9, 200])
+def test_a_value_that_is_not_finite_makes_its_block_nan(fmt, bad, m):
+    """Its block's scale is the format's NaN in both directions, so its row of a product is NaN and its token's
+    column of a weight gradient too; every other block is as without it."""
+    require_cuda()
+    f, b, k, n = FORMATS[fmt], ref.BLOCK[fmt], 160, 80
+    row, col = m // 2, 70
+    x = workloads.bf16_to_f32(_x(m, k, 3))
+    x[row, col] = 1.0
+    clean = to_dev(workloads.f32_to_bf16(x))
+    x[row, col] = bad
+    dirty = clean.clone()
+    dirty[row, col] = bad
+    nan = 255 if fmt == "mxfp4" else 0x7F
+    q, s, qT, sT = fb.fp8blk_quantize_mx4(dirty, f, fb.BOTH)
+    q1, s1, _, _ = fb.fp8blk_quantize_mx4(dirty, f, fb.ROWWISE)
+    c, t, cT, tT = fb.fp8blk_quantize_mx4(clean, f, fb.BOTH)
+    assert torch.equal(s, s1) and torch.equal(q, q1)
+    for got, want, r, at, codes, clean_codes in ((s, t, row, col, q, c), (sT, tT, col, row, qT, cT)):
+        place = (r // 128, at // b // 4, (r % 32) * 16 + (r % 128 // 32) * 4 + at // b % 4)
+        assert int(got[place]) == nan
+        got, want = got.clone(), want.clone()
+        got[place] = want[place] = 0
+        assert torch.equal(got, want)
+        span = slice(at // b * b // 2, (at // b + 1) * b // 2)
+        codes, clean_codes = codes.clone(), clean_codes.clone()
+        codes[r, span] = clean_codes[r, span] = 0
+        assert torch.equal(codes, clean_codes)
+    y = fb.fp8blk_dequantize_mx4(q, s, f).float()
+    inside = torch.zeros_like(y, dtype=torch.bool)
+    inside[row, col // b * b:(col // b + 1) * b] = True
+    assert torch.equal(torch.isnan(y), inside)
+    w, dy = to_dev(_x(n, k, 4)), to_dev(_x(m, n, 5))
+    qw, sw, _, _ = fb.fp8blk_quantize_mx4(w, f)
+    d = fb.mx4_linear_forward(dirty, qw, sw, f)
+    dw = fb.mx4_linear_wgrad(dirty, dy, f)
+    assert fb.fp8blk_get_device_error() == 0
+    assert bool(torch.isnan(d[row]).all()) and bool(torch.isnan(dw[:, col]).all())
+    rest = torch.arange(m, device="cuda") != row
+    assert bool(torch.isfinite(d[rest]).all()) and bool(torch.isfinite(dw[:, torch.arange(k, device="cuda") != col]).all())
+    assert torch.equal(d[rest], fb.mx4_linear_forward(clean, qw, sw, f)[rest])
