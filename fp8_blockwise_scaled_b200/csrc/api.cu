@@ -78,13 +78,13 @@ int pdl_enabled() {
   return e ? std::atoi(e) != 0 : 0;
 }
 
-// Rows sorted by group, up to 64 a group on average: dependent launch always.  There
-// the kernels are short enough for their prologues (barriers, tensor memory, the
-// groups' table) to show: 509 rows in 64 groups forward 50.3 -> 45.7 us, 1003 rows in
+// Rows sorted by group, up to 64 a group on average: dependent launch unless FP8BLK_PDL
+// says otherwise.  There the kernels are short enough for their prologues (barriers,
+// tensor memory, the groups' table) to show: 509 rows in 64 groups forward 50.3 -> 45.7 us, 1003 rows in
 // 16 groups backward 78.5 -> 72.1 us; with 1024 rows a group 2% slower, as above.
 // `slack`: padding a group that the rows may hold.
 int grouped_pdl(int64_t rows, int64_t groups, int64_t slack) {
-  return rows <= (64 + slack) * groups ? 1 : pdl_enabled();
+  return std::getenv("FP8BLK_PDL") ? pdl_enabled() : rows <= (64 + slack) * groups;
 }
 
 int env_int(const char* name, int fallback) {

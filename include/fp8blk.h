@@ -43,9 +43,10 @@
  *  - Environment variables, read at every call (tuning and tests only; the
  *    defaults are the measured best on B200):
  *      FP8BLK_WAIT_TIMEOUT_MS     bound of each device-side wait (default 4000)
- *      FP8BLK_PDL=1               launch with programmatic dependent launch (the
- *                                 entry points for rows sorted by group do so
- *                                 without it for few rows a group)
+ *      FP8BLK_PDL                 1: launch with programmatic dependent launch; 0:
+ *                                 never (default, but for the entry points for
+ *                                 rows sorted by group with few rows a group,
+ *                                 which do so where the variable is not set)
  *      FP8BLK_GEMM_BLOCK_N        128 or 256: force the GEMM tile width
  *      FP8BLK_GEMM_PAIR           1: 256x256 tiles on CTA pairs wherever M and
  *                                 N are multiples of 256; 0: never (default)
