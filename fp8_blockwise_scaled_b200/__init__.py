@@ -46,6 +46,7 @@ number of rows in a group):
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -549,6 +550,12 @@ def fp8blk_gemm_grouped(layout, a, sa, b, sb, offsets, d=None, stream=None, out_
     return d
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(size, *args) -> int:
+    """size(*args), remembered: the library's answer depends on nothing else, and asking costs a call of it."""
+    return size(*args)
+
+
 def fp8blk_linear_grouped_workspace_bytes(groups: int, rows: int, k: int) -> int:
     """Bytes of workspace fp8blk_linear_grouped needs for x [rows, k] in `groups` groups (0: none)."""
     return int(lib.fp8blk_linear_grouped_workspace_bytes(int(groups), int(rows), int(k)))
@@ -574,8 +581,9 @@ def fp8blk_linear_grouped(x, qw, sw, offsets, d=None, workspace=None, stream=Non
     if not (qw.is_contiguous() and sw.is_contiguous()):
         raise ValueError("codes and scales must be contiguous")
     if workspace is None:
-        if rows > 16 or rows > 12 * groups:    # else one launch, which needs none
-            workspace = _empty((rows * k + rows * (k // 128) * 4,), torch.uint8, dev)
+        need = _workspace_bytes(fp8blk_linear_grouped_workspace_bytes, groups, rows, k)
+        if need > 0:                           # else one launch, which needs none
+            workspace = _empty((need,), torch.uint8, dev)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     if d is None:
@@ -737,9 +745,9 @@ def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, wo
     if x.shape[1] != k:
         raise ValueError("X and W disagree on their features")
     if workspace is None:
-        if m > 16:                             # else one launch, which needs none
-            blocks, atoms, size = _mx4_scale_shape(fmt, m, k)
-            workspace = _empty((-(-m * k // 32) * 16 + blocks * atoms * size,), torch.uint8, dev)
+        need = _workspace_bytes(fp8blk_linear_mx4_workspace_bytes, fmt, m, k)
+        if need > 0:                           # else one launch, which needs none
+            workspace = _empty((need,), torch.uint8, dev)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     if d is None:
