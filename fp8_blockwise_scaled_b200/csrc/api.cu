@@ -38,6 +38,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 bool dim_ok(int64_t d) { return d > 0 && d % 128 == 0; }
 
+// Every size is compared with this before two of them are multiplied in 64 bits.
+constexpr int64_t kMostSize = int64_t(1) << 31;
+
+// The limits of the ragged quantiser: 32-bit tile counts, and 32-bit offsets inside a
+// tile, of 128 transposed rows (`padded` apart) and of 8 rows in place (`cols` apart).
+bool ragged_quant_ok(int64_t padded, int64_t cols) {
+  return padded >= 0 && padded <= (int64_t(1) << 25) && cols <= (int64_t(1) << 29) &&
+         (padded / 128 + 1) * (cols / 128) < kMostSize;
+}
+
 // The kernels use tcgen05 and TMA features of compute capability 10.0.
 fp8blk_status check_device() {
   static thread_local int cached_dev = -1;
@@ -163,7 +173,7 @@ fp8blk_status fp8blk_quantize_act_1x128(const void* x, int64_t rows, int64_t col
 }
 
 int64_t fp8blk_grouped_padded_rows(int64_t rows, int64_t groups) {
-  if (rows < 0 || groups < 1 || groups > FP8BLK_MAX_GROUPS) return -1;
+  if (rows < 0 || groups < 1 || groups > FP8BLK_MAX_GROUPS || rows > INT64_MAX - 127 * FP8BLK_MAX_GROUPS) return -1;
   return (rows + 127 * (groups < rows ? groups : rows)) / 128 * 128;
 }
 
@@ -174,8 +184,7 @@ fp8blk_status fp8blk_quantize_act_1x128_grouped(const void* x, int64_t rows, int
   if (!offsets || groups < 1 || groups > FP8BLK_MAX_GROUPS) return FP8BLK_ERR_INVALID_ARG;
   if (rows < 0 || !dim_ok(cols)) return FP8BLK_ERR_SHAPE;
   const int64_t padded = fp8blk_grouped_padded_rows(rows, groups);
-  // 32-bit tile counts, and 32-bit offsets inside a tile's 128 transposed rows.
-  if (padded > (int64_t(1) << 25) || (padded / 128 + 1) * (cols / 128) >= (int64_t(1) << 31)) return FP8BLK_ERR_SHAPE;
+  if (!ragged_quant_ok(padded, cols)) return FP8BLK_ERR_SHAPE;
   if (ldx < cols) return FP8BLK_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(offsets) & 3u) return FP8BLK_ERR_ALIGN;
   if (rows == 0) return (mode & ~(FP8BLK_BOTH | FP8BLK_E5M2)) || !(mode & FP8BLK_BOTH) ? FP8BLK_ERR_INVALID_ARG : FP8BLK_OK;
@@ -343,11 +352,11 @@ fp8blk_status grouped_gemm_args(int layout, int64_t groups, const int32_t* offse
   // Ragged: the rows (FWD / DGRAD: M, any number; WGRAD: K, whole 128-token blocks, maybe none).
   if (!dim_ok(N) || (wgrad ? !dim_ok(M) || K < 0 || K % 128 : M < 0 || !dim_ok(K))) return FP8BLK_ERR_SHAPE;
   // 32-bit TMA coordinates and tile counts.
-  constexpr int64_t kMost = int64_t(1) << 31;
+  if (M >= kMostSize || N >= kMostSize || K >= kMostSize) return FP8BLK_ERR_SHAPE;
   const int64_t rows = wgrad ? K : M;
   const int64_t blocks = wgrad ? groups * (M / 128) : M / 128 + groups;
-  if (rows >= kMost - 128 || groups * N >= kMost || (wgrad ? groups * M : groups * K) >= kMost ||
-      blocks * (N / 128) >= kMost - 1024)
+  if (rows >= kMostSize - 128 || groups * N >= kMostSize || (wgrad ? groups * M : groups * K) >= kMostSize ||
+      blocks * (N / 128) >= kMostSize - 1024)
     return FP8BLK_ERR_SHAPE;
   if (ldd < N) return FP8BLK_ERR_INVALID_ARG;
   if (!wgrad && M == 0) {
@@ -411,7 +420,8 @@ fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* off
 }
 
 int64_t fp8blk_linear_grouped_workspace_bytes(int64_t groups, int64_t M, int64_t K) {
-  if (groups < 1 || groups > FP8BLK_MAX_GROUPS || M < 0 || K < 0 || K % 128 != 0) return -1;
+  if (groups < 1 || groups > FP8BLK_MAX_GROUPS || M < 0 || K < 0 || K % 128 != 0 || M >= kMostSize || K >= kMostSize)
+    return -1;
   return fp8blk::grouped_quantizes_on_the_way(M, groups) ? 0 : M * K + M * (K / 128) * 4;
 }
 
@@ -423,9 +433,8 @@ fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* o
   bool nothing;
   fp8blk_status st = grouped_gemm_args(FP8BLK_FWD | format, groups, offsets, M, N, K, w, sw, d, ldd, g, &nothing);
   if (st != FP8BLK_OK || nothing) return st;
-  // The quantiser's limits (fp8blk_quantize_act_1x128_grouped).
   const int64_t padded = fp8blk_grouped_padded_rows(M, groups);
-  if (padded > (int64_t(1) << 25) || (padded / 128 + 1) * (K / 128) >= (int64_t(1) << 31)) return FP8BLK_ERR_SHAPE;
+  if (!ragged_quant_ok(padded, K)) return FP8BLK_ERR_SHAPE;
   const bool one_launch = fp8blk::grouped_quantizes_on_the_way(M, groups);
   if (!x || ldx < K || (!workspace && !one_launch)) return FP8BLK_ERR_INVALID_ARG;
   if (!aligned16(x) || ldx % 8 != 0 || !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
@@ -501,7 +510,8 @@ fp8blk_status fp8blk_gemm_splitk(int layout, int64_t M, int64_t N, int64_t K, co
 }
 
 int64_t fp8blk_mx4_scale_bytes(int format, int64_t rows, int64_t k) {
-  if ((format != FP8BLK_MXFP4 && format != FP8BLK_NVFP4) || rows < 0 || k < 0) return -1;
+  if ((format != FP8BLK_MXFP4 && format != FP8BLK_NVFP4) || rows < 0 || k < 0 || rows >= kMostSize || k >= kMostSize)
+    return -1;
   const int64_t atom = format == FP8BLK_NVFP4 ? 64 : 128;
   return ((rows + 127) / 128) * ((k + atom - 1) / atom) * fp8blk::kMx4AtomBytes;
 }

@@ -152,7 +152,8 @@ fp8blk_status fp8blk_quantize_act_1x128(const void* x, int64_t rows, int64_t col
  *            P = fp8blk_grouped_padded_rows(rows, groups); group e starts at
  *            column 128 * sum over i < e of ceil((offsets[i+1] - offsets[i]) / 128).
  *            What lies behind the last group's last block is left as it was.
- * FP8BLK_ERR_SHAPE for rows so many that P > 2^25; other errors as above.
+ * FP8BLK_ERR_SHAPE for rows so many that P > 2^25, or cols above 2^29; other
+ * errors as above.
  */
 #define FP8BLK_MAX_GROUPS 1024
 fp8blk_status fp8blk_quantize_act_1x128_grouped(const void* x, int64_t rows, int64_t cols, int64_t ldx, int mode,
@@ -161,7 +162,7 @@ fp8blk_status fp8blk_quantize_act_1x128_grouped(const void* x, int64_t rows, int
 
 /* Columns of the padded layout for any split of `rows` rows into `groups` groups:
  * (rows + 127 min(groups, rows)) rounded down to a multiple of 128; -1 for
- * rows < 0 or groups out of range. */
+ * rows < 0, groups out of range or rows that the result cannot count. */
 int64_t fp8blk_grouped_padded_rows(int64_t rows, int64_t groups);
 
 /*
@@ -295,7 +296,7 @@ fp8blk_status fp8blk_gemm_grouped(int layout, int64_t groups, const int32_t* off
  *               caller, overwritten; two calls may share it only if they are ordered
  *               (one stream, or events).
  * Other arguments and errors as for those two calls; the size is -1 for groups out
- * of range, a negative M or K no multiple of 128.
+ * of range, a negative M, K no multiple of 128, or one of them from 2^31 on.
  */
 int64_t fp8blk_linear_grouped_workspace_bytes(int64_t groups, int64_t M, int64_t K);
 fp8blk_status fp8blk_linear_grouped(int format, int64_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
@@ -372,7 +373,7 @@ int fp8blk_gemm_splitk_count(int layout, int64_t M, int64_t N, int64_t K);
  * row r and block j of an atom (128 rows x 4 blocks) at byte
  * (r % 32) * 16 + (r % 128 / 32) * 4 + j; places of rows and blocks that do not
  * exist hold zeros (fp8blk_quantize_mx4 writes them).  fp8blk_mx4_scale_bytes
- * gives the size; -1 for a bad format or a negative size.
+ * gives the size; -1 for a bad format, a negative size or one from 2^31 on.
  */
 typedef enum {
   FP8BLK_MXFP4 = 0,
@@ -437,8 +438,8 @@ fp8blk_status fp8blk_gemm_mx4(int format, int64_t M, int64_t N, int64_t K, const
  *               overwritten; two calls may share it only if they are ordered
  *               (one stream, or events).
  * Other arguments and errors as for those two calls (K a multiple of 32); the
- * size is -1 for a bad format, a negative size or K no multiple of 32 (format
- * without FP8BLK_OUT_F32).
+ * size is -1 for a bad format, a negative size or one from 2^31 on, or K no
+ * multiple of 32 (format without FP8BLK_OUT_F32).
  */
 int64_t fp8blk_linear_mx4_workspace_bytes(int format, int64_t M, int64_t K);
 fp8blk_status fp8blk_linear_mx4(int format, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
