@@ -171,6 +171,12 @@ def _some_missing(mode, q_row, s_row, q_colT, s_colT) -> bool:
                 mode & COLWISE_T and (q_colT is None or s_colT is None))
 
 
+def _same_tokens(x, dy) -> None:
+    """Padded along the tokens, operands of different numbers of them can look alike."""
+    if x.shape[0] != dy.shape[0]:
+        raise ValueError("X and dY disagree on their tokens")
+
+
 def fp8blk_quantize_act_1x128(x, mode=ROWWISE, q_row=None, s_row=None, q_colT=None, s_colT=None,
                               stream=None):
     """Activation quantisation in 1x128 groups.  Returns (q_row, s_row, q_colT, s_colT); unused are None.
@@ -609,6 +615,7 @@ def grouped_linear_forward(x, qw, sw, offsets, stream=None):
 def grouped_linear_backward(x, dy, qwT, swT, offsets, stream=None, out_dtype=torch.bfloat16):
     """(dX [T,in], dW [groups,out,in]) of grouped_linear_forward, both FP8 blockwise; the transposed weights
     come quantised (fp8blk_quantize_weight_128x128_t or _both: qwT [in,groups*out], swT).  out_dtype: dW's."""
+    _same_tokens(x, dy)
     if stream is not None:
         return _on_stream(stream, _need_cuda(x, dy),
                           lambda: grouped_linear_backward(x, dy, qwT, swT, offsets, None, out_dtype))
@@ -776,6 +783,7 @@ def mx4_linear_wgrad(x, dy, fmt, x_scale=None, dy_scale=None, stream=None, out_d
     # The calls of fp8blk_quantize_mx4 (COLWISE_T, twice) and fp8blk_gemm_mx4 with one allocation for the codes
     # and scales between them: with few tokens the host's time is what counts.
     x, dy = _bf16_2d(x), _bf16_2d(dy)
+    _same_tokens(x, dy)
     if fmt not in MX4_BLOCK:
         raise ValueError("fmt must be MXFP4 or NVFP4")
     if out_dtype not in (torch.bfloat16, torch.float32):
@@ -785,8 +793,6 @@ def mx4_linear_wgrad(x, dy, fmt, x_scale=None, dy_scale=None, stream=None, out_d
         return _on_stream(stream, dev, lambda: mx4_linear_wgrad(x, dy, fmt, x_scale, dy_scale, None, out_dtype))
     tokens, k = x.shape
     n = dy.shape[1]
-    if dy.shape[0] != tokens:
-        raise ValueError("X and dY disagree on their tokens")
     padded = -(-tokens // 32) * 32
     at, places = 0, []                     # codes and scales of dY, then of X, all on 16-byte boundaries
     for rows in (n, k):
@@ -809,6 +815,7 @@ def mx4_linear_backward(x, dy, qwT, swT, fmt, x_scale=None, dy_scale=None, w_sca
                         out_dtype=torch.bfloat16):
     """(dX, dW) of Y = X . W^T in 4 bits: dY quantised once along features and along tokens, X along
     tokens, W ahead (fp8blk_quantize_mx4, COLWISE_T).  out_dtype: dW's."""
+    _same_tokens(x, dy)
     if stream is not None:
         return _on_stream(stream, _need_cuda(x, dy), lambda: mx4_linear_backward(x, dy, qwT, swT, fmt, x_scale, dy_scale,
                                                                                  w_scale, None, out_dtype))
