@@ -124,8 +124,9 @@ def _out(t, shape, dtype, device):
 
 
 def _pitch(t, width: int) -> int:
-    """Row pitch of a 2-D (or the last two dimensions of a) tensor; a single row's stride says nothing."""
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), width)
+    """Row pitch of a 2-D (or the last two dimensions of a) tensor; a single row's stride says nothing, so that
+    its pitch is the next one the library takes."""
+    return t.stride(-2) if t.shape[-2] > 1 else -(-width // 8) * 8
 
 
 def _ptr(t) -> int | None:
@@ -724,7 +725,7 @@ def fp8blk_gemm_mx4(a, sa, b, sb, fmt, tensor_sa=None, tensor_sb=None, d=None, s
             d = d[:, :n]
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (m, n) or d.stride(1) != 1:
         raise ValueError("d must be a bfloat16 or float32 [M,N] tensor with unit column stride")
-    pitch = _pitch(d, -(-n // 8) * 8)
+    pitch = _pitch(d, n)
     _run(dev, lib.fp8blk_gemm_mx4, int(fmt) | (OUT_F32 if d.dtype == torch.float32 else 0), m, n, k, _ptr(a), _ptr(sa),
          _ptr(tensor_sa), _ptr(b), _ptr(sb), _ptr(tensor_sb), _ptr(d), pitch, _stream_handle(stream, dev))
     return d
@@ -766,7 +767,7 @@ def fp8blk_linear_mx4(x, qw, sw, fmt, tensor_sx=None, tensor_sw=None, d=None, wo
             d = d[:, :n]
     elif d.dtype not in (torch.bfloat16, torch.float32) or tuple(d.shape) != (m, n) or d.stride(1) != 1:
         raise ValueError("d must be a bfloat16 or float32 [M,N] tensor with unit column stride")
-    pitch, ldx = _pitch(d, -(-n // 8) * 8), _pitch(x, k)
+    pitch, ldx = _pitch(d, n), _pitch(x, k)
     _run(dev, lib.fp8blk_linear_mx4, fmt | (OUT_F32 if d.dtype == torch.float32 else 0), m, n, k, x.data_ptr(), ldx,
          _ptr(tensor_sx), qw.data_ptr(), sw.data_ptr(), _ptr(tensor_sw), _ptr(workspace),
          0 if workspace is None else workspace.numel(), d.data_ptr(), pitch, _stream_handle(stream, dev))

@@ -28,3 +28,29 @@ def test_backward_of_other_numbers_of_tokens(tokens):
     fb.grouped_linear_backward(x, same, q8, s8, off)
     fb.mx4_linear_backward(x, same, q4, s4, fb.MXFP4)
     fb.mx4_linear_wgrad(x, same, fb.MXFP4)
+
+
+def test_single_row_of_any_stride(monkeypatch):
+    """The stride of a matrix of one row says nothing: the library gets a pitch that it takes."""
+    seen = []
+    monkeypatch.setattr(fb, "_run", lambda device, fn, *args: seen.append(args))
+    row = torch.zeros(1, 129, dtype=torch.bfloat16)[:, :128]                     # pitch 129
+    odd = torch.zeros(1, 10, dtype=torch.bfloat16)                               # contiguous, 10 columns
+    q8, s8 = torch.zeros((128, 128), dtype=torch.float8_e4m3fn), torch.zeros((1, 1))
+    q4, s4 = torch.zeros((10, 64), dtype=torch.uint8), torch.zeros((1, 1, 512), dtype=torch.uint8)
+    off = torch.zeros(2, dtype=torch.int32)
+    fb.fp8blk_quantize_act_1x128_grouped(row, off)
+    assert seen.pop()[3] == 128
+    fb.fp8blk_quantize_mx4(row, fb.MXFP4)
+    assert seen.pop()[3] == 128
+    fb.fp8blk_quantize_mx4(odd, fb.MXFP4, fb.COLWISE_T)
+    assert seen.pop()[3] == 16
+    fb.fp8blk_linear_grouped(row, q8, s8, off, d=row)
+    args = seen.pop()
+    assert args[7] == 128 and args[-2] == 128
+    fb.fp8blk_linear_mx4(row, q4, s4, fb.MXFP4, d=odd)
+    args = seen.pop()
+    assert args[5] == 128 and args[-2] == 16
+    wide = torch.zeros(2, 136, dtype=torch.bfloat16)[:, :128]                    # two rows: their own pitch
+    fb.fp8blk_quantize_mx4(wide, fb.MXFP4)
+    assert seen.pop()[3] == 136

@@ -139,3 +139,23 @@ def test_a_value_that_is_not_finite_makes_its_block_nan(fmt, bad, m):
     rest = torch.arange(m, device="cuda") != row
     assert bool(torch.isfinite(d[rest]).all()) and bool(torch.isfinite(dw[:, torch.arange(k, device="cuda") != col]).all())
     assert torch.equal(d[rest], fb.mx4_linear_forward(clean, qw, sw, f)[rest])
+
+
+@pytest.mark.parametrize("cols", [10, 96])
+def test_single_row_of_any_stride(cols):
+    """A row without a pitch, in and out; what stands beside it stays."""
+    require_cuda()
+    k = 64
+    x = _x(1, 96, 6)[:, :cols]
+    around = torch.full((cols + 3,), 7.0, dtype=torch.bfloat16, device="cuda")
+    row = around[:cols].reshape(1, cols)
+    row.copy_(to_dev(x))
+    _, _, qT, sT = fb.fp8blk_quantize_mx4(row, fb.MXFP4, fb.COLWISE_T)
+    codes, byte = ref.quantize(np.ascontiguousarray(ref.pad_rows(workloads.bf16_to_f32(x).astype(np.float64)).T), "mxfp4")
+    assert np.array_equal(sT.cpu().numpy(), ref.tile(byte)) and np.array_equal(ref.unpack(qT.cpu().numpy()), codes)
+    w, v = to_dev(_x(cols, k, 7) if cols % 8 == 0 else _x(16, k, 7)[:cols]), to_dev(_x(1, k, 8))
+    qw, sw, _, _ = fb.fp8blk_quantize_mx4(w, fb.MXFP4)
+    want = fb.fp8blk_linear_mx4(v, qw, sw, fb.MXFP4)
+    fb.fp8blk_linear_mx4(v, qw, sw, fb.MXFP4, d=row)
+    assert fb.fp8blk_get_device_error() == 0
+    assert torch.equal(row, want) and bool((around[cols:] == 7.0).all())
