@@ -72,12 +72,11 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
 }
 
-// Scale byte of a block of maximum amax, and what its values are divided by.  g
-// and rg = RN(1 / g): the tensor's scale.  amax / 6 and that by g are correctly
-// rounded by Markstein's correction, as x / s in qmath.cuh: q0 = RN(a y) with y
-// the correctly rounded reciprocal, then RN(q0 + RN(a - q0 b) y).
-// The scale byte of an NVFP4 block of maximum amax.  Below 128 whatever g holds (a
-// scale has no sign, and the byte is an index into a table of 128).
+// The scale byte of an NVFP4 block of maximum amax; g and rg = RN(1 / g): the tensor's
+// scale.  amax / 6 and that by g are correctly rounded by Markstein's correction, as
+// x / s in qmath.cuh: q0 = RN(a y) with y the correctly rounded reciprocal, then
+// RN(q0 + RN(a - q0 b) y).  Below 128 whatever g holds (a scale has no sign, and the
+// byte is an index into a table of 128).
 __device__ __forceinline__ uint32_t nvfp4_scale(float amax, float g, float rg) {
   constexpr float kSixth = 0x1.555556p-3f;              // RN(1 / 6)
   const float a0 = amax * kSixth, a = fmaf(fmaf(-6.0f, a0, amax), kSixth, a0);
@@ -107,6 +106,8 @@ __device__ __forceinline__ uint32_t finish_codes(uint32_t codes, float nr) {
   return (codes ^ 0x88888888u) & keep;
 }
 
+// Scale byte of a block of maximum amax, and what its values are divided by (NVFP4) or
+// multiplied with (MXFP4: q.nr alone).
 template <bool kNv>
 __device__ __forceinline__ uint32_t block_scale(float amax, float g, float rg, QScale& q) {
   if constexpr (kNv) {

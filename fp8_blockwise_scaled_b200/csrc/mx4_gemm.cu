@@ -10,9 +10,8 @@
 // TMEM by tcgen05.cp, in the order of the MMAs that read them.  Two sets of
 // scale columns alternate; a set is rewritten once the MMAs that read it have
 // completed (their commit).  Measured against it on 8192^3: four warps that
-// write the scales with tcgen05.st run MXFP4 equally fast (207 us) and NVFP4
-// slower (250 us instead of 222 us), copies of half the size one step ahead of
-// the MMAs 320 us.
+// write the scales with tcgen05.st run MXFP4 equally fast and NVFP4 12% slower,
+// copies of half the size one step ahead of the MMAs 58% slower.
 //
 // Warp roles (256 threads): warp 0 loads, warp 1 owns TMEM and issues copies
 // and MMAs, warps 4-7 drain the accumulators (two of them alternate, so a
@@ -52,18 +51,20 @@ struct Mx4Params {
   int inject_stall;
 };
 
-template <int BN, bool kNv>
+constexpr int kBN = 128;                 // columns of gemm_mx4_kernel's tile: one block of scale rows
+
+template <bool kNv>
 struct MxCfg {
   static constexpr int kAtoms = kNv ? 4 : 2;              // scale atoms of 128 rows in a stage
   static constexpr int kABytes = 128 * 128;
-  static constexpr int kBBytes = BN * 128;
+  static constexpr int kBBytes = kBN * 128;
   static constexpr int kSfBytes = kAtoms * kMx4AtomBytes;    // of each operand
   static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
   static constexpr int kStages = 5;
   static constexpr int kOutBytes = 4 * 2 * 4096;          // two 32-row boxes of 128 bytes for each epilogue warp
   static constexpr int kSetCols = 2 * kAtoms * 4;         // TMEM columns of one set of scales
-  static constexpr int kTmemUsed = 2 * BN + 2 * kSetCols;
-  static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : (kTmemUsed <= 256 ? 256 : 512);
+  static constexpr int kTmemCols = 512;                   // a power of two that holds two accumulators and two sets
+  static_assert(2 * kBN + 2 * kSetCols <= kTmemCols && 2 * kBN + 2 * kSetCols > kTmemCols / 2, "tensor memory");
   static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
 };
 
@@ -77,9 +78,9 @@ struct MxCtrl {
   int abort;
 };
 
-template <int BN, bool kNv>
+template <bool kNv>
 constexpr int mx_smem_bytes() {
-  using C = MxCfg<BN, kNv>;
+  using C = MxCfg<kNv>;
   return 1024 + C::kStages * C::kStageBytes + C::kOutBytes + static_cast<int>(sizeof(MxCtrl));
 }
 
@@ -169,18 +170,18 @@ __device__ __forceinline__ void store_chunk(const Mx4Params& p, const CUtensorMa
 
 }  // namespace
 
-template <int BN, bool kNv>
+template <bool kNv>
 __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_mx4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                     const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
                     const __grid_constant__ CUtensorMap tm_d, const Mx4Params p) {
-  using C = MxCfg<BN, kNv>;
+  using C = MxCfg<kNv>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smem_out = smem + C::kStages * C::kStageBytes;
   MxCtrl* ctrl = reinterpret_cast<MxCtrl*>(smem_out + C::kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int num_mb = static_cast<int>((p.M + 127) / 128), num_nb = static_cast<int>((p.N + BN - 1) / BN);
+  const int num_mb = static_cast<int>((p.M + 127) / 128), num_nb = static_cast<int>((p.N + kBN - 1) / kBN);
   const int kblocks = static_cast<int>((p.K + kStageK - 1) / kStageK);
   const int tiles = num_mb * num_nb;
 
@@ -233,10 +234,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           uint64_t* full = &ctrl->full[st.idx];
           mbar_arrive_expect_tx(full, C::kStageBytes);
           tma_load_2d(stage, &tm_a, full, kb * 128, mb * 128);
-          tma_load_2d(stage + C::kABytes, &tm_b, full, kb * 128, nb * BN);
+          tma_load_2d(stage + C::kABytes, &tm_b, full, kb * 128, nb * kBN);
           // Scale maps: rows of 128-row blocks, columns of 8-byte words, 64 to an atom.
           tma_load_2d(stage + C::kABytes + C::kBBytes, &tm_sa, full, kb * C::kAtoms * 64, mb);
-          tma_load_2d(stage + C::kABytes + C::kBBytes + C::kSfBytes, &tm_sb, full, kb * C::kAtoms * 64, nb * BN / 128);
+          tma_load_2d(stage + C::kABytes + C::kBBytes + C::kSfBytes, &tm_sb, full, kb * C::kAtoms * 64, nb);
           ++issued;
           st.next();
         }
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one();
-    constexpr uint32_t idesc = idesc_mx4(128, BN, kNv);
+    constexpr uint32_t idesc = idesc_mx4(128, kBN, kNv);
     const uint32_t smem0 = smem_addr(smem);
     Ring<C::kStages> st;
     Ring<2> acc, set;
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       if (!__all_sync(0xFFFFFFFFu,
                       mbar_wait_hot(&ctrl->tempty[acc.idx], acc.phase ^ 1u, abort, 0, p.timeout_ns, p.err)))
         break;
-      const uint32_t d_tmem = tmem_base + acc.idx * BN;
+      const uint32_t d_tmem = tmem_base + acc.idx * kBN;
       for (int kb = 0; kb < kblocks; ++kb) {
         const bool got = mbar_wait_hot(&ctrl->full[st.idx], st.phase, abort, 0, p.timeout_ns, p.err) &&
                          mbar_wait_hot(&ctrl->sfree[set.idx], set.phase ^ 1u, abort, 0, p.timeout_ns, p.err);
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         const uint64_t adesc = smem_desc_kmajor_sw128(a_addr);
         const uint64_t bdesc = smem_desc_kmajor_sw128(a_addr + C::kABytes);
         const uint64_t sfdesc = smem_desc_atom(sf_addr);
-        const uint32_t sfa = tmem_base + 2 * BN + set.idx * C::kSetCols, sfb = sfa + C::kAtoms * 4;
+        const uint32_t sfa = tmem_base + 2 * kBN + set.idx * C::kSetCols, sfb = sfa + C::kAtoms * 4;
         const int steps = static_cast<int>(min((p.K - static_cast<int64_t>(kb) * kStageK + 63) / 64, int64_t{4}));
         if (leader) {
 #pragma unroll
@@ -318,13 +319,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                       mbar_wait_bounded(&ctrl->tfull[acc.idx], acc.phase, abort, p.timeout_ns, p.err)))
         break;
       tc_fence_after_sync();
-      const uint32_t taddr = lanes + acc.idx * BN;
+      const uint32_t taddr = lanes + acc.idx * kBN;
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 64) {
+      for (int c = 0; c < kBN; c += 64) {
         uint32_t r[2][32];
         load_chunk(taddr + c, r);
         store_chunk<2>(p, &tm_d, stg, r, alpha, static_cast<int64_t>(mb) * 128 + quarter * 32,
-                       static_cast<int64_t>(nb) * BN + c, lane, stores);
+                       static_cast<int64_t>(nb) * kBN + c, lane, stores);
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -359,8 +360,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 //
 // What bounds it: power.  A stage takes 735 (MXFP4) or 768 cycles (NVFP4) where
 // its MMAs alone take 512, but the SMs run at 1.6 GHz under it, and variants that
-// need fewer cycles ran at lower clocks for the same time.  8192^3: 206 us, 5.3
-// PFLOP/s (MXFP4), 222 us (NVFP4).  With K = 1536 another 1500 cycles a tile go
+// need fewer cycles ran at lower clocks for the same time.  8192^3 alone: 211 to 213
+// us, 5.2 PFLOP/s (MXFP4), 222 to 227 us (NVFP4); call after call 240 us at a median
+// of 1.56 GHz, 258 us at 1.51.  With K = 1536 another 1500 cycles a tile go
 // to the hand-over between tiles.
 namespace {
 
@@ -931,17 +933,17 @@ Mx4Params mx_params(const Mx4GemmArgs& g, int64_t num_mb) {
   return p;
 }
 
-template <int BN, bool kNv>
+template <bool kNv>
 cudaError_t launch_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
   static PerContext<int> smem_set;
-  constexpr int kSmem = mx_smem_bytes<BN, kNv>();
+  constexpr int kSmem = mx_smem_bytes<kNv>();
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_kernel<BN, kNv>, kSmem); e != cudaSuccess) return e;
+  if (cudaError_t e = set_smem_once(smem_set, gemm_mx4_kernel<kNv>, kSmem); e != cudaSuccess) return e;
   CUtensorMap ta, tb, tsa, tsb, td;
-  if (!codes_map(&ta, g.a, g.M, g.K, 128) || !codes_map(&tb, g.b, g.N, g.K, BN) ||
+  if (!codes_map(&ta, g.a, g.M, g.K, 128) || !codes_map(&tb, g.b, g.N, g.K, kBN) ||
       !scales_map(&tsa, g.sa, g.M, g.K, kNv, 1) || !scales_map(&tsb, g.sb, g.N, g.K, kNv, 1) || !mx_out_map(&td, g))
     return cudaErrorInvalidValue;
-  const int64_t num_mb = (g.M + 127) / 128, num_nb = (g.N + BN - 1) / BN;
+  const int64_t num_mb = (g.M + 127) / 128, num_nb = (g.N + kBN - 1) / kBN;
   const Mx4Params p = mx_params(g, num_mb);
   int64_t ctas = num_sms();
   if (g.max_ctas > 0 && g.max_ctas < ctas) ctas = g.max_ctas;
@@ -954,7 +956,7 @@ cudaError_t launch_mx4(const Mx4GemmArgs& g, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   cfg.numAttrs = set_pdl_attr(attr, g.pdl);
   cfg.attrs = attr;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<BN, kNv>, ta, tb, tsa, tsb, td, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<kNv>, ta, tb, tsa, tsb, td, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -977,7 +979,7 @@ cudaError_t launch_mx4_few(const Mx4GemmArgs& g, const FewInput& in, cudaStream_
   while (splits < 8 && 2 * splits * tiles <= 2 * num_sms() && kblocks >= 4 * splits) splits *= 2;
   // It is not persistent: a cap on the CTAs is kept by the 1-CTA kernel.
   if constexpr (!kQuant) {
-    if (g.max_ctas > 0 && tiles * splits > g.max_ctas) return launch_mx4<128, kNv>(g, stream);
+    if (g.max_ctas > 0 && tiles * splits > g.max_ctas) return launch_mx4<kNv>(g, stream);
   }
   const Mx4Params p = mx_params(g, 1);
   cudaLaunchConfig_t cfg = {};
@@ -1034,10 +1036,10 @@ cudaError_t launch_mx4_fmt(const Mx4GemmArgs& g, cudaStream_t stream) {
   if (g.M <= 32) return launch_mx4_few<32, kNv, false>(g, {}, stream);
   if (g.M <= 64) return launch_mx4_few<64, kNv, false>(g, {}, stream);
   const int64_t pair_tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-  // Pairs once there is a tile for every pair of SMs (16384 x 17920 x 1536 NVFP4: 243 us, in 128 x 128 tiles 333 us;
-  // 1536 x 8960 x 16384 MXFP4: 84 us and 162 us).
+  // Pairs once there is a tile for every pair of SMs (alone; 16384 x 17920 x 1536 NVFP4: 234 to 238 us, in 128 x 128
+  // tiles 396 us; 1536 x 8960 x 16384 MXFP4: 92 to 94 us and 187 us).
   if (pair_tiles >= num_sms() / 2 && g.max_ctas != 1) return launch_mx4_pair<kNv>(g, stream);
-  return launch_mx4<128, kNv>(g, stream);
+  return launch_mx4<kNv>(g, stream);
 }
 
 }  // namespace

@@ -21,8 +21,8 @@
 // atoms' order, and the transposed codes as 64-byte lines (16-byte chunks XORed
 // with the column block, two lanes a bank).  Per element 2 B read, 1/2 B of codes
 // and 1/32 or 1/16 B of scales written per direction: HBM bound in one direction
-// (16384 x 8960: 66 us MXFP4, 69 to 75 us NVFP4, 5.0 to 5.7 TB/s), bound by the code
-// arithmetic in both (93 us and 122 us; 20 instructions an element at 60% of the
+// (16384 x 8960: 66 us MXFP4, 70 to 78 us NVFP4, 4.8 to 5.6 TB/s), bound by the code
+// arithmetic in both (96 us and 127 us; 20 instructions an element at 60% of the
 // issue slots).
 #include <cudaTypedefs.h>
 
