@@ -159,3 +159,28 @@ def test_single_row_of_any_stride(cols):
     fb.fp8blk_linear_mx4(v, qw, sw, fb.MXFP4, d=row)
     assert fb.fp8blk_get_device_error() == 0
     assert torch.equal(row, want) and bool((around[cols:] == 7.0).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("m", [64, 256])
+def test_product_of_every_scale_byte(fmt, m):
+    """1.0 in one place a row below every scale byte, the smallest and the subnormal ones among them: D is the
+    product of two scales exactly, wherever fp32 holds it as a normal number."""
+    require_cuda()
+    k, n = 64, 4
+    b = ref.BLOCK[fmt]
+    one, none = np.array([56 if fmt == "nvfp4" else 127], np.uint8), np.uint8(0)
+    last = 127 if fmt == "nvfp4" else 255
+    for first in range(0, last, m):
+        mine = (np.arange(first, first + m) % last).astype(np.uint8)
+        ca, ba = np.zeros((m, k), np.uint8), np.full((m, k // b), none)
+        place = (np.arange(m) * 7) % k
+        ca[np.arange(m), place] = 2
+        ba[np.arange(m), place // b] = mine
+        bb = np.repeat(np.array([one[0], 1, last - 1, last // 3], np.uint8)[:, None], k // b, 1)
+        d = fb.fp8blk_gemm_mx4(_dev8(ref.pack(ca)), _dev8(ref.tile(ba)), _dev8(ref.pack(np.full((n, k), 2, np.uint8))),
+                               _dev8(ref.tile(bb)), FORMATS[fmt], out_dtype=torch.float32).cpu().numpy()
+        want = ref.values(ca, ba, fmt) @ ref.values(np.full((n, k), 2, np.uint8), bb, fmt).T
+        held = (want == 0) | ((want >= 2.0**-126) & (want < 2.0**128))
+        assert held.any() and np.array_equal(d[held], want[held].astype(np.float32))
+    assert fb.fp8blk_get_device_error() == 0
