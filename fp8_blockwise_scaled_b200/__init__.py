@@ -274,6 +274,8 @@ def fp8blk_gemm(layout, a, sa, b, sb, d=None, stream=None, out_dtype=torch.bfloa
     want_sb = (k // 128, n) if layout == WGRAD else (n // 128, k // 128)
     if tuple(sa.shape) != (k // 128, m) or tuple(sb.shape) != want_sb:
         raise ValueError(f"scale shapes {tuple(sa.shape)}, {tuple(sb.shape)} do not match layout {layout}")
+    if sa.dtype != torch.float32 or sb.dtype != torch.float32:
+        raise ValueError("scales must be float32")
     if not (a.is_contiguous() and b.is_contiguous() and sa.is_contiguous() and sb.is_contiguous()):
         raise ValueError("operands and scales must be contiguous")
     if d is None:
@@ -400,7 +402,7 @@ def fp8blk_amax_ema_static(x, amax, scale, stream=None):
 def fp8blk_quantize_tensor(x, scale, q=None, stream=None):
     """The whole tensor with its one scale (device float32 [1]).  Returns q [rows, cols] E4M3."""
     x = _bf16_2d(x)
-    dev = _need_cuda(x, scale, q)
+    dev = _need_cuda(x, _tensor_scale(scale), q)
     if stream is not None and q is None:
         return _on_stream(stream, dev, lambda: fp8blk_quantize_tensor(x, scale))
     rows, cols = x.shape
@@ -418,8 +420,13 @@ def fp8blk_gemm_tensor_scaled(a, sa, b, sb, d=None, stream=None):
     n = b.shape[0]
     if b.shape[1] != k or a.dtype != E4M3 or b.dtype != E4M3:
         raise ValueError("A [M,K] and B [N,K] must be float8_e4m3fn")
+    if not (a.is_contiguous() and b.is_contiguous()):
+        raise ValueError("operands must be contiguous")
+    _tensor_scale(sa), _tensor_scale(sb)
     if d is None:
         d = torch.empty((m, n), dtype=torch.bfloat16, device=a.device)
+    elif d.dtype != torch.bfloat16 or tuple(d.shape) != (m, n) or d.stride(1) != 1:
+        raise ValueError("d must be a bfloat16 [M,N] tensor with unit column stride")
     _run(dev, lib.fp8blk_gemm_tensor_scaled, m, n, k, _ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(d), d.stride(0),
                                         _stream_handle(stream, dev))
     return d

@@ -54,3 +54,24 @@ def test_single_row_of_any_stride(monkeypatch):
     wide = torch.zeros(2, 136, dtype=torch.bfloat16)[:, :128]                    # two rows: their own pitch
     fb.fp8blk_quantize_mx4(wide, fb.MXFP4)
     assert seen.pop()[3] == 136
+
+
+def test_per_tensor_calls_refuse_what_the_kernels_would_read_or_write_wrongly():
+    """Shapes, types and strides that reach the kernel as bare pointers."""
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    q, one = torch.zeros((128, 128), dtype=f8), torch.ones(1)
+    x = torch.zeros((128, 128), dtype=torch.bfloat16)
+    fb.fp8blk_gemm_tensor_scaled(q, one, q, one, d=torch.zeros((128, 256), dtype=torch.bfloat16)[:, :128])
+    fb.fp8blk_quantize_tensor(x, one)
+    wide = torch.zeros((128, 256), dtype=f8)[:, :128]
+    for call in (lambda: fb.fp8blk_gemm_tensor_scaled(wide, one, q, one), lambda: fb.fp8blk_gemm_tensor_scaled(q, one, wide, one),
+                 lambda: fb.fp8blk_gemm_tensor_scaled(q, one.half(), q, one),
+                 lambda: fb.fp8blk_gemm_tensor_scaled(q, one, q, torch.ones(0)),
+                 lambda: fb.fp8blk_gemm_tensor_scaled(q, one, q, one, d=torch.zeros((128, 64), dtype=torch.bfloat16)),
+                 lambda: fb.fp8blk_gemm_tensor_scaled(q, one, q, one, d=torch.zeros((128, 128))),
+                 lambda: fb.fp8blk_gemm_tensor_scaled(q, one, q, one, d=x.t()),
+                 lambda: fb.fp8blk_quantize_tensor(x, one.half()), lambda: fb.fp8blk_quantize_tensor(x, torch.ones(0)),
+                 lambda: fb.fp8blk_gemm(fb.FWD, q, torch.ones(1, 128).half(), q, torch.ones(1, 1)),
+                 lambda: fb.fp8blk_gemm(fb.FWD, q, torch.ones(1, 128), q, torch.ones(1, 1).half())):
+        with pytest.raises(ValueError):
+            call()
